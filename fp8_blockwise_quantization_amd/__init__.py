@@ -5,8 +5,10 @@ quantization, the blockwise-scaled FP8 GEMM and its grouped-expert (MoE) form, a
 FP8 for attention Q/K/V and the KV cache with recalibrated scales, and the quantizers and GEMM
 of the FP8 backward pass (transposed weight copy, 128x1 token groups, row-scaled GEMM), and the
 GEMMs with the activation quantization fused in (dense, and grouped with the codes read through
-the router's token indices). Tensors live on the GPU; the functions only marshal arguments into
-the C ABI (include/fp8rl.h).
+the router's token indices), and the operators between the linears: residual addition with
+root-mean-square norm and 1x128 codes, the experts' sort, dispatch and combine, and the rotated
+append to a paged KV cache. Tensors live on the GPU; the functions only marshal arguments into
+the C ABI (include/fp8rl.h, include/fp8rl_block.h).
 """
 
 from ._lib import (  # noqa: F401
@@ -54,6 +56,20 @@ from ._lib import (  # noqa: F401
     lib,
     new_workspace,
 )
+from ._block import (  # noqa: F401
+    EXPORTED_BLOCK,
+    FP8RL_IDS_I32,
+    FP8RL_IDS_I64,
+    fp8rl_add_rmsnorm_bwd,
+    fp8rl_add_rmsnorm_bwd_workspace_bytes,
+    fp8rl_add_rmsnorm_quant,
+    fp8rl_moe_combine,
+    fp8rl_moe_combine_bwd,
+    fp8rl_moe_dispatch,
+    fp8rl_moe_sort,
+    fp8rl_moe_sort_workspace_bytes,
+    fp8rl_rope_kv_append,
+)
 
 # Short aliases.
 quant_weight = fp8rl_quant_weight_blk128
@@ -73,3 +89,10 @@ quant_per_tensor_batched = fp8rl_quant_bf16_per_tensor_batched
 quant_weight_t = fp8rl_quant_weight_blk128_t
 quant_colwise = fp8rl_quant_act_colwise128
 gemm_rowscaled = fp8rl_gemm_w8a8_rowscaled
+add_rmsnorm_quant = fp8rl_add_rmsnorm_quant
+add_rmsnorm_bwd = fp8rl_add_rmsnorm_bwd
+moe_sort = fp8rl_moe_sort
+moe_dispatch = fp8rl_moe_dispatch
+moe_combine = fp8rl_moe_combine
+moe_combine_bwd = fp8rl_moe_combine_bwd
+rope_kv_append = fp8rl_rope_kv_append

@@ -20,9 +20,10 @@ Sources (the pages this follows, cited by title and section):
 
 Modules: ``e4m3`` (codec), ``quant`` (the two quantizers), ``gemm`` (dequantized fp64 GEMM and its
 grouped-expert form), ``backward`` (the FP8 input- and weight-gradient GEMMs and the quantizations
-they need) and ``kvcache`` (per-tensor Q/K/V scale recalibration and the FP8 KV-cache store).
+they need), ``kvcache`` (per-tensor Q/K/V scale recalibration and the FP8 KV-cache store) and
+``block`` (the norm, expert and cache-append operators between the linears).
 Every function with no independent pin would say "parity unpinned"; none does at present (see the
 tests under ``tests/test_oracle_*.py``).
 """
 
-from . import backward, e4m3, gemm, kvcache, quant  # noqa: F401
+from . import backward, block, e4m3, gemm, kvcache, quant  # noqa: F401
