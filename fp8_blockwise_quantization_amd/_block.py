@@ -8,9 +8,9 @@ stream, or on ``stream``.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import functools
-import inspect
+import struct
 
 import torch
 
@@ -70,7 +70,7 @@ def declare_block(L: ctypes.CDLL) -> ctypes.CDLL:
         "fp8rl_moe_combine": (ci, [vp, ci, i64, i64, vp, vp, i64, i32, i64, vp, ci, i64, vp]),
         "fp8rl_moe_combine_bwd": (ci, [vp, i64, vp, i64, ci, i64, vp, vp, i64, i32, i64, vp, i64,
                                        vp, vp]),
-        "fp8rl_rope_kv_append": (ci, [ctypes.POINTER(RopeKvArgs), vp]),
+        "fp8rl_rope_kv_append": (ci, [vp, vp]),  # the struct by reference or as its bytes
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -78,6 +78,10 @@ def declare_block(L: ctypes.CDLL) -> ctypes.CDLL:
         f.argtypes = args
     return L
 
+
+# RopeKvArgs as struct.pack lays it out (native alignment, like the C struct): filling bytes costs a
+# fraction of filling a ctypes structure.
+_pack_rope = struct.Struct("@PPPqqqqiiiiifPPqPPPqPPPPPPqiqqq").pack
 
 _L = None
 
@@ -89,34 +93,30 @@ def _block_lib() -> ctypes.CDLL:
     return _L
 
 
-def _on_device(fn):
-    """Run `fn` with its first tensor's device current and, where `stream` is given, that stream as
-    torch's current one (so that what the call allocates belongs to it)."""
-    names = list(inspect.signature(fn).parameters)
-    idx = names.index("stream")
-
-    @functools.wraps(fn)
-    def wrapper(*args, **kwargs):
-        t = args[0] if args else kwargs.get(names[0])
-        if t is None:
-            t = args[1] if len(args) > 1 else kwargs.get(names[1])
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{names[0]} must be a device (cuda) tensor")
-        if t.get_device() != torch.cuda.current_device():
-            with torch.cuda.device(t.get_device()):
-                return wrapper(*args, **kwargs)
-        stream = args[idx] if len(args) > idx else kwargs.get("stream")
-        if stream is None:
-            return fn(*args, **kwargs)
-        with _on_stream(stream):
-            return fn(*args, **kwargs)
-
-    return wrapper
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
 
 
-def _raw_stream(dev: int) -> int:
-    # torch's current stream of the device: `stream` itself under _on_device
-    return torch.cuda.current_stream(dev).cuda_stream
+@contextlib.contextmanager
+def _at(t, name, stream):
+    """Make t's device current and, where `stream` is given, that stream torch's current one (so
+    that what the call allocates belongs to it)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device (cuda) tensor")
+    with torch.cuda.device(t.get_device()), _on_stream(stream):
+        if torch.cuda.current_device() != t.get_device():
+            raise ValueError(f"stream belongs to another device than {name}")
+        yield
+
+
+def _here(t, stream) -> int:
+    """The device of a call's first tensor where the call can run as things stand; else -1 (a
+    stream was given, or the device is not the current one, or t is no device tensor)."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    return dev if stream is None and dev >= 0 and dev == _device() else -1
+
+
+# The address of the device's current stream in torch (`stream` itself under _at).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _fail(name, t, dtype, shape, dev):
@@ -132,20 +132,38 @@ def _fail(name, t, dtype, shape, dev):
                      "no matrix of rows)")
 
 
-def _matrix(t, name, dtype, rows, cols, dev):
+def _matrix(t, name, dtype, shape, dev):
     """(address, row pitch) of a [rows][cols] matrix with unit column stride."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == dev
-            and t.shape == (rows, cols) and (t.stride(1) == 1 or cols <= 1)):
-        _fail(name, t, dtype, (rows, cols), dev)
-    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+    try:
+        stride = t.stride()
+        if (t.dtype is dtype and t.get_device() == dev and t.shape == shape
+                and (stride[1] == 1 or shape[1] <= 1)):
+            return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
+    except AttributeError:  # no tensor
+        pass
+    _fail(name, t, dtype, shape, dev)
 
 
 def _vector(t, name, dtype, shape, dev):
     """Address of a contiguous tensor."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == dev
-            and t.shape == shape and t.is_contiguous()):
-        _fail(name, t, dtype, shape, dev)
-    return t.data_ptr()
+    try:
+        if (t.dtype is dtype and t.get_device() == dev and t.shape == shape
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _fail(name, t, dtype, shape, dev)
+
+
+def _flat(t, name, dtype, n, dev):
+    """Address of a contiguous tensor of n values."""
+    try:
+        if (t.dtype is dtype and t.get_device() == dev and t.numel() == n
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _fail(name, t, dtype, (n,), dev)
 
 
 def _workspace(workspace, need, dev):
@@ -176,7 +194,6 @@ def _is_2d(t, name):
 # ------------------------------------------------------------------------------------------ norm
 
 
-@_on_device
 def fp8rl_add_rmsnorm_quant(x, weight, residual=None, eps=1e-6, h=None, y=None, xq=None, sa=None,
                             rows: bool = False, codes: bool = True, scale="fp32", stream=None):
     """Residual addition, root-mean-square norm and 1x128 quantization of bf16 x [M][K].
@@ -185,31 +202,35 @@ def fp8rl_add_rmsnorm_quant(x, weight, residual=None, eps=1e-6, h=None, y=None, 
     rows (None with ``codes=False``), the bf16 stream h = x + residual (None without ``residual``)
     and the bf16 normalised rows y (with ``rows=True`` or a tensor ``y``; else None). ``h`` may be
     ``x`` or ``residual`` itself. ``scale`` is 'fp32' or 'pow2'."""
-    bf16, dev = torch.bfloat16, x.get_device()
+    dev = _here(x, stream)
+    if dev < 0:
+        with _at(x, "x", stream):
+            return fp8rl_add_rmsnorm_quant(x, weight, residual, eps, h, y, xq, sa, rows, codes, scale)
+    bf16 = torch.bfloat16
     M, K = _is_2d(x, "x")
-    px, ld_x = _matrix(x, "x", bf16, M, K, dev)
-    pw = _vector(weight, "weight", bf16, (K,), dev)
+    px, ld_x = _matrix(x, "x", bf16, (M, K), dev)
+    pw = _flat(weight, "weight", bf16, K, dev)
     pr = ph = py = pq = ps = None
     ld_r = ld_h = ld_y = ld_q = 0
     if residual is not None:
-        pr, ld_r = _matrix(residual, "residual", bf16, M, K, dev)
+        pr, ld_r = _matrix(residual, "residual", bf16, (M, K), dev)
         if h is None:
             h = torch.empty((M, K), dtype=bf16, device=x.device)
     if h is not None:
-        ph, ld_h = _matrix(h, "h", bf16, M, K, dev)
+        ph, ld_h = _matrix(h, "h", bf16, (M, K), dev)
     if rows and y is None:
         y = torch.empty((M, K), dtype=bf16, device=x.device)
     if y is not None:
-        py, ld_y = _matrix(y, "y", bf16, M, K, dev)
+        py, ld_y = _matrix(y, "y", bf16, (M, K), dev)
     if codes or xq is not None or sa is not None:
         if xq is None:
             xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
         if sa is None:
             sa = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
-        pq, ld_q = _matrix(xq, "xq", torch.uint8, M, K, dev)
+        pq, ld_q = _matrix(xq, "xq", torch.uint8, (M, K), dev)
         ps = _vector(sa, "sa", torch.float32, (M, K // 128), dev)
     _check(_block_lib().fp8rl_add_rmsnorm_quant(px, ld_x, pr, ld_r, pw, eps, M, K, ph, ld_h, py,
-                                                ld_y, pq, ld_q, ps, _scale_code(scale),
+                                                ld_y, pq, ld_q, ps, 0 if scale == "fp32" else _scale_code(scale),
                                                 _raw_stream(dev)), "fp8rl_add_rmsnorm_quant")
     return xq, sa, h, y
 
@@ -218,25 +239,28 @@ def fp8rl_add_rmsnorm_bwd_workspace_bytes(M: int, K: int) -> int:
     return int(_block_lib().fp8rl_add_rmsnorm_bwd_workspace_bytes(M, K))
 
 
-@_on_device
 def fp8rl_add_rmsnorm_bwd(dy, h, weight, dh=None, eps=1e-6, dx=None, dw=None,
                           weight_grad: bool = True, workspace=None, stream=None):
     """Backward pass of the norm: (dx, dw) from the gradient dy at its output, the stream h it was
     taken of and, if any, the gradient dh that reaches the stream from behind. dx (bf16 [M][K]) is
     the gradient of x and of residual; it may be written in place of dy or dh. dw is float32 [K]
     (None with ``weight_grad=False``)."""
-    bf16, dev = torch.bfloat16, dy.get_device()
+    dev = _here(dy, stream)
+    if dev < 0:
+        with _at(dy, "dy", stream):
+            return fp8rl_add_rmsnorm_bwd(dy, h, weight, dh, eps, dx, dw, weight_grad, workspace)
+    bf16 = torch.bfloat16
     M, K = _is_2d(dy, "dy")
-    pg, ld_g = _matrix(dy, "dy", bf16, M, K, dev)
-    ph, ld_h = _matrix(h, "h", bf16, M, K, dev)
-    pw = _vector(weight, "weight", bf16, (K,), dev)
-    pd, ld_d = _matrix(dh, "dh", bf16, M, K, dev) if dh is not None else (None, 0)
+    pg, ld_g = _matrix(dy, "dy", bf16, (M, K), dev)
+    ph, ld_h = _matrix(h, "h", bf16, (M, K), dev)
+    pw = _flat(weight, "weight", bf16, K, dev)
+    pd, ld_d = _matrix(dh, "dh", bf16, (M, K), dev) if dh is not None else (None, 0)
     if dx is None:
         dx = torch.empty((M, K), dtype=bf16, device=dy.device)
-    px, ld_x = _matrix(dx, "dx", bf16, M, K, dev)
+    px, ld_x = _matrix(dx, "dx", bf16, (M, K), dev)
     if dw is None and weight_grad:
         dw = torch.empty(K, dtype=torch.float32, device=dy.device)
-    po = _vector(dw, "dw", torch.float32, (K,), dev) if dw is not None else None
+    po = _flat(dw, "dw", torch.float32, K, dev) if dw is not None else None
     L = _block_lib()
     need = L.fp8rl_add_rmsnorm_bwd_workspace_bytes(M, K) if dw is not None else 0
     keep, ws, nbytes = _workspace(workspace, need, dev)
@@ -252,14 +276,16 @@ def fp8rl_moe_sort_workspace_bytes(T: int, top_k: int, E: int) -> int:
     return int(_block_lib().fp8rl_moe_sort_workspace_bytes(T, top_k, E))
 
 
-@_on_device
 def fp8rl_moe_sort(topk_ids, E: int, expert_offsets=None, row_ids=None, pos=None, workspace=None,
                    stream=None):
     """The router's choices topk_ids [T][top_k] (int32 or int64, contiguous; an id outside [0, E)
     is another rank's) in expert order: int32 (expert_offsets [E + 1], row_ids [T * top_k],
     pos [T][top_k]). expert_offsets and row_ids are what the grouped GEMMs read; pos is the grouped
     row of each choice, -1 where it has none."""
-    dev = topk_ids.get_device()
+    dev = _here(topk_ids, stream)
+    if dev < 0:
+        with _at(topk_ids, "topk_ids", stream):
+            return fp8rl_moe_sort(topk_ids, E, expert_offsets, row_ids, pos, workspace)
     T, k = _is_2d(topk_ids, "topk_ids")
     if topk_ids.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"topk_ids must be torch.int32 or torch.int64, got {topk_ids.dtype}")
@@ -271,8 +297,8 @@ def fp8rl_moe_sort(topk_ids, E: int, expert_offsets=None, row_ids=None, pos=None
         row_ids = torch.empty(T * k, dtype=i32, device=device)
     if pos is None:
         pos = torch.empty((T, k), dtype=i32, device=device)
-    po = _vector(expert_offsets, "expert_offsets", i32, (E + 1,), dev)
-    pr = _vector(row_ids, "row_ids", i32, (T * k,), dev)
+    po = _flat(expert_offsets, "expert_offsets", i32, E + 1, dev)
+    pr = _flat(row_ids, "row_ids", i32, T * k, dev)
     pp = _vector(pos, "pos", i32, (T, k), dev)
     L = _block_lib()
     keep, ws, nbytes = _workspace(workspace, L.fp8rl_moe_sort_workspace_bytes(T, k, E), dev)
@@ -282,62 +308,68 @@ def fp8rl_moe_sort(topk_ids, E: int, expert_offsets=None, row_ids=None, pos=None
     return expert_offsets, row_ids, pos
 
 
-@_on_device
 def fp8rl_moe_dispatch(x, pos, out=None, stream=None):
     """Token rows moved into expert order: out[pos[t][j]] = x[t]. ``out`` (bf16 [R][N]) is
     allocated with a row per choice when not given; rows that no choice names are not written."""
-    dev = x.get_device()
+    dev = _here(x, stream)
+    if dev < 0:
+        with _at(x, "x", stream):
+            return fp8rl_moe_dispatch(x, pos, out)
     T, N = _is_2d(x, "x")
     k = _is_2d(pos, "pos")[1]
-    px, ld_x = _matrix(x, "x", torch.bfloat16, T, N, dev)
+    px, ld_x = _matrix(x, "x", torch.bfloat16, (T, N), dev)
     pp = _vector(pos, "pos", torch.int32, (T, k), dev)
     if out is None:
         out = torch.empty((T * k, N), dtype=torch.bfloat16, device=x.device)
     R = _is_2d(out, "out")[0]
-    po, ld_o = _matrix(out, "out", torch.bfloat16, R, N, dev)
+    po, ld_o = _matrix(out, "out", torch.bfloat16, (R, N), dev)
     _check(_block_lib().fp8rl_moe_dispatch(px, ld_x, pp, T, k, N, po, R, ld_o, _raw_stream(dev)),
            "fp8rl_moe_dispatch")
     return out
 
 
-@_on_device
 def fp8rl_moe_combine(y, pos, weights=None, out_dtype=torch.bfloat16, out=None, stream=None):
     """out[t] = sum over j of weights[t][j] * y[pos[t][j]] (bf16 or float32 y [R][N], float32
     weights [T][top_k] or None for ones); choices without a row (pos < 0) add nothing."""
-    dev = y.get_device()
+    dev = _here(y, stream)
+    if dev < 0:
+        with _at(y, "y", stream):
+            return fp8rl_moe_combine(y, pos, weights, out_dtype, out)
     R, N = _is_2d(y, "y")
     T, k = _is_2d(pos, "pos")
     kind = _out_type(y, "y")
-    py, ld_y = _matrix(y, "y", y.dtype, R, N, dev)
+    py, ld_y = _matrix(y, "y", y.dtype, (R, N), dev)
     pp = _vector(pos, "pos", torch.int32, (T, k), dev)
     pw = _vector(weights, "weights", torch.float32, (T, k), dev) if weights is not None else None
     if out is None:
         out = torch.empty((T, N), dtype=out_dtype, device=y.device)
     out_kind = _out_type(out, "out")
-    po, ld_o = _matrix(out, "out", out.dtype, T, N, dev)
+    po, ld_o = _matrix(out, "out", out.dtype, (T, N), dev)
     _check(_block_lib().fp8rl_moe_combine(py, kind, R, ld_y, pp, pw, T, k, N, po, out_kind, ld_o,
                                           _raw_stream(dev)), "fp8rl_moe_combine")
     return out
 
 
-@_on_device
 def fp8rl_moe_combine_bwd(dout, y, pos, weights=None, dy=None, dweights=None, R=None,
                           y_dtype=torch.bfloat16, stream=None):
     """Gradients of fp8rl_moe_combine: (dy, dweights) from bf16 dout [T][N]. dy[pos[t][j]] =
     weights[t][j] * dout[t] in y's type (rows that no choice names are not written); dweights
     float32 [T][top_k]. With ``y=None`` only dy is formed, [R][N] of ``y_dtype`` (R: a row per
     choice unless given). dy may be written in place of y."""
-    dev = dout.get_device()
+    dev = _here(dout, stream)
+    if dev < 0:
+        with _at(dout, "dout", stream):
+            return fp8rl_moe_combine_bwd(dout, y, pos, weights, dy, dweights, R, y_dtype)
     T, N = _is_2d(dout, "dout")
     k = _is_2d(pos, "pos")[1]
-    pg, ld_g = _matrix(dout, "dout", torch.bfloat16, T, N, dev)
+    pg, ld_g = _matrix(dout, "dout", torch.bfloat16, (T, N), dev)
     pp = _vector(pos, "pos", torch.int32, (T, k), dev)
     pw = _vector(weights, "weights", torch.float32, (T, k), dev) if weights is not None else None
     py = pd = None
     ld_y = 0
     if y is not None:
         R, y_dtype = _is_2d(y, "y")[0], y.dtype
-        py, ld_y = _matrix(y, "y", y_dtype, R, N, dev)
+        py, ld_y = _matrix(y, "y", y_dtype, (R, N), dev)
         if dweights is None:
             dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device)
         pd = _vector(dweights, "dweights", torch.float32, (T, k), dev)
@@ -349,7 +381,7 @@ def fp8rl_moe_combine_bwd(dout, y, pos, weights=None, dy=None, dweights=None, R=
         R, y_dtype = _is_2d(dy, "dy")[0], dy.dtype
     R = dy.shape[0] if R is None else R
     kind = _out_type(dy, "dy")
-    po, ld_o = _matrix(dy, "dy", y_dtype, R, N, dev)
+    po, ld_o = _matrix(dy, "dy", y_dtype, (R, N), dev)
     _check(_block_lib().fp8rl_moe_combine_bwd(pg, ld_g, py, ld_y, kind, R, pp, pw, T, k, N, po,
                                               ld_o, pd, _raw_stream(dev)), "fp8rl_moe_combine_bwd")
     return dy, dweights
@@ -358,13 +390,19 @@ def fp8rl_moe_combine_bwd(dout, y, pos, weights=None, dy=None, dweights=None, R=
 # -------------------------------------------------------------------------------------- KV cache
 
 
-def _scalar(t, name, dev):
-    if not (t.dtype == torch.float32 and t.get_device() == dev and t.numel() == 1):
-        _fail(name, t, torch.float32, (1,), dev)
-    return t.data_ptr()
+def _cache(t, name, dtype, shape, strides, dev):
+    """Address of a cache view of the first one's shape and strides."""
+    try:
+        if (t.dtype is dtype and t.get_device() == dev and t.shape == shape
+                and (strides[3] == 1 or shape[3] <= 1)):
+            if t.stride() != strides and shape[0] > 0:
+                raise ValueError("k_cache and v_cache must have the same strides")
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _fail(name, t, dtype, shape, dev)
 
 
-@_on_device
 def fp8rl_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out=None,
                          interleaved: bool = False, q_weight=None, k_weight=None, eps=1e-6,
                          q_scale=None, k_scale=None, v_scale=None, stream=None):
@@ -378,52 +416,56 @@ def fp8rl_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_c
     laid out head by head): bf16, or uint8 for E4M3 codes with device scalars ``k_scale`` and
     ``v_scale``. A token with a negative slot stores nothing. ``q_out`` is bf16 (it may be q), or
     uint8 codes with ``q_scale``; q may be None (k and v alone). ``cos_sin`` None rotates nothing."""
-    bf16, dev = torch.bfloat16, k.get_device()
+    dev = _here(k, stream)
+    if dev < 0:
+        with _at(k, "k", stream):
+            return fp8rl_rope_kv_append(
+                q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, interleaved,
+                q_weight, k_weight, eps, q_scale, k_scale, v_scale)
+    bf16 = torch.bfloat16
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be 4-D: [page][place][head][column]")
     pages, page, Hkv, D = k_cache.shape
     T = _is_2d(k, "k")[0]
-    pk, ld_k = _matrix(k, "k", bf16, T, Hkv * D, dev)
-    pv, ld_v = _matrix(v, "v", bf16, T, Hkv * D, dev)
+    pk, ld_k = _matrix(k, "k", bf16, (T, Hkv * D), dev)
+    pv, ld_v = _matrix(v, "v", bf16, (T, Hkv * D), dev)
     kind = bf16 if k_scale is None else torch.uint8
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not (c.dtype == kind and c.get_device() == dev and c.shape == k_cache.shape
-                and (c.stride(3) == 1 or D <= 1)):
-            _fail(name, c, kind, (pages, page, Hkv, D), dev)
     strides = k_cache.stride()
-    if pages > 0 and v_cache.stride() != strides:
-        raise ValueError("k_cache and v_cache must have the same strides")
+    pkc = _cache(k_cache, "k_cache", kind, k_cache.shape, strides, dev)
+    pvc = _cache(v_cache, "v_cache", kind, k_cache.shape, strides, dev)
     # a dimension of one entry has no stride to speak of
     page_stride = strides[0] if pages > 1 else 0
     slot_stride = strides[1] if page > 1 else D
     head_stride = strides[2] if Hkv > 1 else D
-    pq = po = None
-    ld_q = ld_o = Hq = 0
+    pq = po = ld_q = ld_o = Hq = 0
     if q is not None:
         cols = _is_2d(q, "q")[1]
         if D == 0 or cols % D:
             raise ValueError(f"q has {cols} columns, no multiple of the head width {D}")
         Hq = cols // D
-        pq, ld_q = _matrix(q, "q", bf16, T, cols, dev)
+        pq, ld_q = _matrix(q, "q", bf16, (T, cols), dev)
         q_kind = bf16 if q_scale is None else torch.uint8
         if q_out is None:
             q_out = torch.empty((T, cols), dtype=q_kind, device=k.device)
-        po, ld_o = _matrix(q_out, "q_out", q_kind, T, cols, dev)
-    rot = max_pos = 0
-    pc = pp = None
+        po, ld_o = _matrix(q_out, "q_out", q_kind, (T, cols), dev)
+    rot = max_pos = pc = pp = qw = kw = qs = ks = vs = 0
     if cos_sin is not None:
         max_pos, rot = _is_2d(cos_sin, "cos_sin")
         pc = _vector(cos_sin, "cos_sin", torch.float32, (max_pos, rot), dev)
-        pp = _vector(positions, "positions", torch.int64, (T,), dev)
-    ps = _vector(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
-    qw = _vector(q_weight, "q_weight", bf16, (D,), dev) if q_weight is not None else None
-    kw = _vector(k_weight, "k_weight", bf16, (D,), dev) if k_weight is not None else None
-    qs = _scalar(q_scale, "q_scale", dev) if q_scale is not None else None
-    ks = _scalar(k_scale, "k_scale", dev) if k_scale is not None else None
-    vs = _scalar(v_scale, "v_scale", dev) if v_scale is not None else None
-    args = RopeKvArgs(pq, pk, pv, ld_q, ld_k, ld_v, T, Hq, Hkv, D, rot, 1 if interleaved else 0,
-                      eps, pp, pc, max_pos, qw, kw, po, ld_o, qs, ps, k_cache.data_ptr(),
-                      v_cache.data_ptr(), ks, vs, pages, page, page_stride, slot_stride,
-                      head_stride)
+        pp = _flat(positions, "positions", torch.int64, T, dev)
+    ps = _flat(slot_mapping, "slot_mapping", torch.int64, T, dev)
+    if q_weight is not None:
+        qw = _flat(q_weight, "q_weight", bf16, D, dev)
+    if k_weight is not None:
+        kw = _flat(k_weight, "k_weight", bf16, D, dev)
+    if q_scale is not None:
+        qs = _flat(q_scale, "q_scale", torch.float32, 1, dev)
+    if k_scale is not None:
+        ks = _flat(k_scale, "k_scale", torch.float32, 1, dev)
+    if v_scale is not None:
+        vs = _flat(v_scale, "v_scale", torch.float32, 1, dev)
+    args = _pack_rope(pq, pk, pv, ld_q, ld_k, ld_v, T, Hq, Hkv, D, rot, 1 if interleaved else 0,
+                      eps, pp, pc, max_pos, qw, kw, po, ld_o, qs, ps, pkc, pvc, ks, vs, pages,
+                      page, page_stride, slot_stride, head_stride)
     _check(_block_lib().fp8rl_rope_kv_append(args, _raw_stream(dev)), "fp8rl_rope_kv_append")
     return q_out

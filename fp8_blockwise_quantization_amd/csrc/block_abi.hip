@@ -145,6 +145,8 @@ fp8rl_status fp8rl_moe_dispatch(const uint16_t* x, int64_t ld_x, const int32_t* 
   if (fp8rl_status s = check_rows(x, ld_x, N)) return s;
   if (fp8rl_status s = check_rows(out, ld_out, N)) return s;
   if (!aligned(pos, 4)) return FP8RL_ERR_ALIGN;
+  // a wave per 2048 values of a row, below 2^32 threads in a grid
+  if (T * ((N + 2047) / 2048) >= (int64_t{1} << 26)) return FP8RL_ERR_SHAPE;
   fp8rl::MoeArgs a{};
   a.x = x, a.out = out, a.pos = pos;
   a.ld_x = ld_x, a.ld_out = ld_out;
@@ -202,8 +204,8 @@ fp8rl_status fp8rl_rope_kv_append(const fp8rl_rope_kv_args* args, void* stream) 
     return FP8RL_ERR_SHAPE;
   if (a.head_dim < 8 || a.head_dim > 512 || a.head_dim % 8) return FP8RL_ERR_SHAPE;
   if (a.rot_dim < 0 || a.rot_dim > a.head_dim || a.rot_dim % 16) return FP8RL_ERR_SHAPE;
-  // up to 32 threads per head of a token, below 2^32 in a grid
-  if (a.T * (a.q_heads + 2 * (int64_t)a.kv_heads) >= (int64_t{1} << 26)) return FP8RL_ERR_SHAPE;
+  // up to 32 threads per head of a token in whole waves, below 2^32 in a grid
+  if (a.T * (a.q_heads + 2 * (int64_t)a.kv_heads) >= (int64_t{1} << 25)) return FP8RL_ERR_SHAPE;
   if (a.interleaved != 0 && a.interleaved != 1) return FP8RL_ERR_ARG;
   if (a.page_size < 1 || a.num_pages >= (int64_t{1} << 62) / a.page_size) return FP8RL_ERR_SHAPE;
   if ((!a.q_weight) != (!a.k_weight) || (!a.k_scale) != (!a.v_scale)) return FP8RL_ERR_NULL;

@@ -91,17 +91,29 @@ __device__ __forceinline__ u32x4 round8(const float (&f)[8]) {
                pack2_bf16(f[6], f[7])};
 }
 
-// Clamp to the finite E4M3 range, keeping NaN (the conversion then gives a NaN code).
-__device__ __forceinline__ float clamp_e4m3_nan(float t) {
-  return __builtin_fabsf(t) > kE4M3Max ? __builtin_copysignf(kE4M3Max, t) : t;
+// E4M3 codes of 8 float32 values, saturating; a NaN gives a NaN code. The clamp is one median of
+// three; it loses a NaN, so values among which there is one (four unordered comparisons tell) go
+// through a select instead.
+__device__ __forceinline__ u32x2 encode8(float (&t)[8]) {
+  const bool nan = __builtin_isunordered(t[0], t[1]) | __builtin_isunordered(t[2], t[3]) |
+                   __builtin_isunordered(t[4], t[5]) | __builtin_isunordered(t[6], t[7]);
+  if (nan) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      t[i] = __builtin_fabsf(t[i]) > kE4M3Max ? __builtin_copysignf(kE4M3Max, t[i]) : t[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = clamp_e4m3(t[i]);
+  }
+  return u32x2{pack4_e4m3(t[0], t[1], t[2], t[3]), pack4_e4m3(t[4], t[5], t[6], t[7])};
 }
 
 // The E4M3 codes of f * r, the product formed in float64 and rounded through float32.
 __device__ __forceinline__ u32x2 codes8(const float (&f)[8], double r) {
   float t[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = clamp_e4m3_nan((float)((double)f[i] * r));
-  return u32x2{pack4_e4m3(t[0], t[1], t[2], t[3]), pack4_e4m3(t[4], t[5], t[6], t[7])};
+  for (int i = 0; i < 8; ++i) t[i] = (float)((double)f[i] * r);
+  return encode8(t);
 }
 
 // Sum over the 64 lanes of a wave, the same bits in every lane.

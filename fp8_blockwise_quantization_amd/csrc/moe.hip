@@ -17,13 +17,13 @@ namespace fp8rl {
 // the second one sums for itself.
 // ---------------------------------------------------------------------------------------------
 constexpr int kSortWaves = 16;
-constexpr int64_t kSortOne = 16384;
-constexpr int64_t kSortBlock = 8192;
+constexpr int kSortLoads = 4;  // choices a lane has in flight and keeps: a wave's tile is 256
+constexpr int64_t kSortOne = 64 * kSortLoads * kSortWaves;  // choices of one workgroup: one tile each
 constexpr int64_t kSortMostBlocks = 256;
 
 int64_t sort_blocks(int64_t n) {
   if (n <= kSortOne) return 1;
-  const int64_t b = (n + kSortBlock - 1) / kSortBlock;
+  const int64_t b = (n + kSortOne - 1) / kSortOne;
   return b < kSortMostBlocks ? b : kSortMostBlocks;
 }
 
@@ -35,21 +35,27 @@ int64_t sort_piece(int64_t n, int64_t blocks) {
   return ((n + waves - 1) / waves + 63) / 64 * 64;
 }
 
-// The expert of choice i, or E (counted nowhere) when it has none.
+// The experts of a wave's choices i0 + 64 j + lane, E (counted nowhere) for one without an expert
+// or past the end.
 template <typename ID>
-__device__ __forceinline__ int expert_of(const ID* __restrict__ ids, int64_t i, int64_t end, int E) {
-  if (i >= end) return E;
-  const ID e = ids[i];
-  return e >= 0 && e < (ID)E ? (int)e : E;
+__device__ __forceinline__ void load_tile(const ID* __restrict__ ids, int64_t i0, int64_t end,
+                                          int E, int (&e)[kSortLoads]) {
+  ID id[kSortLoads];
+#pragma unroll
+  for (int j = 0; j < kSortLoads; ++j) {
+    const int64_t i = i0 + 64 * j + (threadIdx.x & 63);
+    id[j] = -1;
+    if (i < end) id[j] = ids[i];
+  }
+#pragma unroll
+  for (int j = 0; j < kSortLoads; ++j) e[j] = id[j] >= 0 && id[j] < (ID)E ? (int)id[j] : E;
 }
 
-template <typename ID>
-__device__ __forceinline__ void count_piece(const ID* __restrict__ ids, int64_t begin, int64_t end,
-                                            int E, int* cnt) {
-  for (int64_t i = begin + (threadIdx.x & 63); i < end; i += 64) {
-    const int e = expert_of(ids, i, end, E);
-    if (e < E) atomicAdd(&cnt[e], 1);  // integers: any order gives the same count
-  }
+// Integers: the counts are the same in any order of the additions.
+__device__ __forceinline__ void count_tile(const int (&e)[kSortLoads], int E, int* cnt) {
+#pragma unroll
+  for (int j = 0; j < kSortLoads; ++j)
+    if (e[j] < E) atomicAdd(&cnt[e[j]], 1);
 }
 
 }  // namespace
@@ -59,13 +65,19 @@ __global__ __launch_bounds__(1024) void moe_count_kernel(const ID* __restrict__ 
                                                          int64_t piece, int E,
                                                          int32_t* __restrict__ counts) {
   extern __shared__ int cnt[];  // [E]
-  for (int e = threadIdx.x; e < E; e += 1024) cnt[e] = 0;
-  __syncthreads();
   const int64_t begin = ((int64_t)blockIdx.x * kSortWaves + (threadIdx.x >> 6)) * piece;
   const int64_t end = begin + piece < n ? begin + piece : n;
-  count_piece(ids, begin, end, E, cnt);
+  int e[kSortLoads];
+  load_tile(ids, begin, end, E, e);
+  for (int i = threadIdx.x; i < E; i += 1024) cnt[i] = 0;
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 1024) counts[(int64_t)blockIdx.x * E + e] = cnt[e];
+  count_tile(e, E, cnt);
+  for (int64_t i0 = begin + 64 * kSortLoads; i0 < end; i0 += 64 * kSortLoads) {
+    load_tile(ids, i0, end, E, e);
+    count_tile(e, E, cnt);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < E; i += 1024) counts[(int64_t)blockIdx.x * E + i] = cnt[i];
 }
 
 // counts: [gridDim.x][E] of moe_count_kernel, or null for a single block.
@@ -79,27 +91,34 @@ __global__ __launch_bounds__(1024) void moe_place_kernel(const ID* __restrict__ 
   extern __shared__ int cnt[];  // [kSortWaves][E]
   __shared__ int wave_total[kSortWaves];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  for (int i = t; i < kSortWaves * E; i += 1024) cnt[i] = 0;
-  __syncthreads();
   const int64_t begin = ((int64_t)blockIdx.x * kSortWaves + wave) * piece;
   const int64_t end = begin + piece < n ? begin + piece : n;
   int* mine = cnt + wave * E;
-  count_piece(ids, begin, end, E, mine);
-  __syncthreads();
+  int e[kSortLoads];
+  load_tile(ids, begin, end, E, e);
 
-  // thread e: expert e's choices in this block (by wave), in earlier blocks and in all
+  // expert t's choices in earlier blocks and in all
   int total = 0, before = 0;
-  if (t < E) {
-    if (counts) {
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int c = counts[(int64_t)b * E + t];
-        total += c;
-        before += b < (int)blockIdx.x ? c : 0;
-      }
-    } else {
-      for (int w = 0; w < kSortWaves; ++w) total += cnt[w * E + t];
+  if (counts && t < E) {
+#pragma unroll 8
+    for (int b = 0; b < (int)gridDim.x; ++b) {
+      const int c = counts[(int64_t)b * E + t];
+      total += c;
+      before += b < (int)blockIdx.x ? c : 0;
     }
   }
+  for (int i = t; i < kSortWaves * E; i += 1024) cnt[i] = 0;
+  __syncthreads();
+  count_tile(e, E, mine);
+  for (int64_t i0 = begin + 64 * kSortLoads; i0 < end; i0 += 64 * kSortLoads) {
+    int more[kSortLoads];
+    load_tile(ids, i0, end, E, more);
+    count_tile(more, E, mine);
+  }
+  __syncthreads();
+  if (!counts && t < E)
+    for (int w = 0; w < kSortWaves; ++w) total += cnt[w * E + t];
+
   // exclusive prefix of the totals over the experts
   int incl = total;
 #pragma unroll
@@ -129,21 +148,25 @@ __global__ __launch_bounds__(1024) void moe_place_kernel(const ID* __restrict__ 
   }
   __syncthreads();
 
-  for (int64_t i0 = begin; i0 < end; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const int e = expert_of(ids, i, end, E);
-    uint64_t same = ~0ull;
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t set = __ballot((e >> b) & 1);
-      same &= (e >> b) & 1 ? set : ~set;
-    }
-    const int below = __popcll(same & ((1ull << lane) - 1));
-    int at = 0;
-    if (below == 0 && e < E) at = atomicAdd(&mine[e], (int)__popcll(same));
-    at = __shfl(at, __ffsll((unsigned long long)same) - 1, 64) + below;
-    if (i < end) {
-      pos[i] = e < E ? at : -1;
-      if (e < E) row_ids[at] = (int)((unsigned)i / (unsigned)top_k);
+  for (int64_t i0 = begin; i0 < end; i0 += 64 * kSortLoads) {
+    if (i0 != begin) load_tile(ids, i0, end, E, e);
+#pragma unroll
+    for (int j = 0; j < kSortLoads; ++j) {
+      if (i0 + 64 * j >= end) break;
+      const int64_t i = i0 + 64 * j + lane;
+      uint64_t same = ~0ull;
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((e[j] >> b) & 1);
+        same &= (e[j] >> b) & 1 ? set : ~set;
+      }
+      const int below = __popcll(same & ((1ull << lane) - 1));
+      int at = 0;
+      if (below == 0 && e[j] < E) at = atomicAdd(&mine[e[j]], (int)__popcll(same));
+      at = __shfl(at, __ffsll((unsigned long long)same) - 1, 64) + below;
+      if (i < end) {
+        pos[i] = e[j] < E ? at : -1;
+        if (e[j] < E) row_ids[at] = (int)((unsigned)i / (unsigned)top_k);
+      }
     }
   }
   // no row behind the last expert's
@@ -183,134 +206,254 @@ hipError_t launch_moe_sort(const void* ids, bool wide, int64_t n, int top_k, int
 }
 
 // ---------------------------------------------------------------------------------------------
-// Rows. 8 values per lane and chunk. A value type is float or uint16_t (bf16).
+// Rows. A workgroup owns a token; a lane owns chunks of 8 values of the row. A value type Y or O is
+// float or uint16_t (bf16).
+//
+// The choices of a token that have a grouped row are found once per wave: lane j reads pos[t][j],
+// a ballot marks the live ones, and their rows (and weights) are read out of the lanes in increasing
+// order into scalar registers. Rows are then loaded S at a time without a branch between the loads,
+// so that all of them are in flight; places past the last live choice load its row again and are
+// taken out of the result by a select, never by a zero weight, which would let a NaN through.
 // ---------------------------------------------------------------------------------------------
 namespace {
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
-  widen8(__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)), f);
-}
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  typedef float f32x4 __attribute__((ext_vector_type(4)));
-  const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
-  const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// 8 values as they lie in memory: what a load in flight occupies.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  u32x4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  }
+  __device__ __forceinline__ void widen(float (&f)[8]) const { widen8(v, f); }
+};
+template <>
+struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+    b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
+  }
+  __device__ __forceinline__ void widen(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+};
+
 __device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) {
-  *reinterpret_cast<u32x4*>(p) = round8(f);
+  __builtin_nontemporal_store(round8(f), reinterpret_cast<u32x4*>(p));
 }
 __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  __builtin_nontemporal_store((f32x4{f[0], f[1], f[2], f[3]}), reinterpret_cast<f32x4*>(p));
+  __builtin_nontemporal_store((f32x4{f[4], f[5], f[6], f[7]}), reinterpret_cast<f32x4*>(p) + 1);
 }
 
-constexpr int kAtOnce = 8;  // choices whose rows are in flight together
+// A token's live choices, held across the lanes of a wave.
+struct Choices {
+  int row;         // lane j: grouped row of choice j
+  float weight;    // lane j: its weight
+  uint64_t live;   // lanes with a row in [0, R)
+  __device__ __forceinline__ void read(const MoeArgs& a, int64_t t) {
+    const int lane = threadIdx.x & 63;
+    row = -1;
+    weight = 1.f;
+    if (lane < a.top_k) {
+      row = a.pos[t * a.top_k + lane];
+      if (a.weights) weight = a.weights[t * a.top_k + lane];
+    }
+    live = __ballot(row >= 0 && row < a.R);
+  }
+};
+
+// The next S live choices out of `left` (which loses them): lane numbers, the last one repeated.
+template <int S>
+__device__ __forceinline__ int take(uint64_t& left, int (&lane)[S]) {
+  int n = 0, last = 0;
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    if (left) last = __ffsll((unsigned long long)left) - 1, ++n;
+    left &= left - 1;  // 0 stays 0: 0 & anything
+    lane[j] = last;
+  }
+  return n;
+}
+
+template <int S, typename Y>
+__device__ __forceinline__ void combine_step(const MoeArgs& a, const Choices& ch, uint64_t& left,
+                                             int c, float (&acc)[8]) {
+  int lane[S];
+  const int n = take<S>(left, lane);
+  Raw8<Y> f[S];
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    const int64_t p = __builtin_amdgcn_readlane(ch.row, lane[j]);
+    f[j].load(static_cast<const Y*>(a.x) + p * a.ld_x + c * 8);
+  }
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    const float w = __uint_as_float(
+        (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(ch.weight), lane[j]));
+    float v[8];
+    f[j].widen(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = j < n ? __builtin_fmaf(w, v[k], acc[k]) : acc[k];
+  }
+}
 
 }  // namespace
 
-// One token per workgroup: its row is read once and written to each of its grouped rows.
-__global__ __launch_bounds__(256) void moe_dispatch_kernel(MoeArgs a) {
-  const int64_t t = blockIdx.x;
-  const uint16_t* x = static_cast<const uint16_t*>(a.x) + t * a.ld_x;
-  uint16_t* out = static_cast<uint16_t*>(a.out);
-  const int32_t* __restrict__ pos = a.pos + t * a.top_k;
-  for (int c = threadIdx.x; c < a.nc; c += blockDim.x) {
-    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x) + c);
-    for (int j = 0; j < a.top_k; ++j) {
-      const int64_t p = pos[j];
-      if (p >= 0 && p < a.R)
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + p * a.ld_out) + c);
-    }
+// A wave takes a block of 64 CH chunks of one token's row, reads it once and writes it to each of
+// the token's grouped rows.
+template <int CH>
+__global__ __launch_bounds__(256) void moe_dispatch_kernel(MoeArgs a, int pieces) {
+  const unsigned w = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const unsigned t = w / (unsigned)pieces;
+  if (t >= a.T) return;
+  const int c0 = (int)(w - t * pieces) * (64 * CH) + (int)(threadIdx.x & 63);
+  const u32x4* x =
+      reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + (int64_t)t * a.ld_x);
+  u32x4 v[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    v[i] = u32x4{0u, 0u, 0u, 0u};
+    if (c0 + 64 * i < a.nc) v[i] = __builtin_nontemporal_load(x + c0 + 64 * i);
+  }
+  Choices ch;
+  ch.read(a, t);
+  for (uint64_t left = ch.live; left; left &= left - 1) {
+    const int64_t p = __builtin_amdgcn_readlane(ch.row, __ffsll((unsigned long long)left) - 1);
+    u32x4* out = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + p * a.ld_out) + c0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (c0 + 64 * i < a.nc) __builtin_nontemporal_store(v[i], out + 64 * i);
   }
 }
 
 template <typename Y, typename O>
 __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
   const int64_t t = blockIdx.x;
-  const Y* y = static_cast<const Y*>(a.x);
-  O* out = static_cast<O*>(a.out) + t * a.ld_out;
-  const int32_t* __restrict__ pos = a.pos + t * a.top_k;
-  const float* __restrict__ w = a.weights ? a.weights + t * a.top_k : nullptr;
+  Choices ch;
+  ch.read(a, t);
   for (int c = threadIdx.x; c < a.nc; c += blockDim.x) {
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
-      float f[kAtOnce][8];
-      float wj[kAtOnce];
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int64_t p = j0 + j < a.top_k ? pos[j0 + j] : -1;
-        const bool live = p >= 0 && p < a.R;  // uniform
-        wj[j] = live ? (w ? w[j0 + j] : 1.f) : 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[j][k] = 0.f;
-        if (live) load8(y + p * a.ld_x + c * 8, f[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(wj[j], f[j][k], acc[k]);
+    for (uint64_t left = ch.live; left;) {
+      const int n = __popcll(left);
+      if (n > 4)
+        combine_step<8, Y>(a, ch, left, c, acc);
+      else if (n > 2)
+        combine_step<4, Y>(a, ch, left, c, acc);
+      else
+        combine_step<2, Y>(a, ch, left, c, acc);
     }
-    store8(out + c * 8, acc);
+    store8(static_cast<O*>(a.out) + t * a.ld_out + c * 8, acc);
   }
 }
 
+namespace {
+
+// Sums of S values over the 64 lanes of a wave: each exchange between lanes l and l ^ o halves the
+// number of values a lane holds, so S values cost S - 1 + log2(64 / S) exchanges instead of 6 S.
+// Returns the sum of value (lane / (64 / S)) in every lane.
+template <int S>
+__device__ __forceinline__ float wave_sums(float (&v)[S]) {
+  const int lane = threadIdx.x & 63;
+  int o = 32;
+#pragma unroll
+  for (int n = S; n > 1; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float keep = up ? v[i + n / 2] : v[i], give = up ? v[i] : v[i + n / 2];
+      v[i] = keep + __shfl_xor(give, o, 64);
+    }
+  }
+  float s = v[0];
+#pragma unroll
+  for (; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  return s;
+}
+
+// S live choices of the token: their rows' products with dout, and their gradients.
+template <int S, typename Y>
+__device__ __forceinline__ void combine_bwd_step(const MoeArgs& a, const Choices& ch,
+                                                 uint64_t& left, int64_t t, float (*red)[8]) {
+  int lane[S];
+  const int n = take<S>(left, lane);
+  const uint16_t* dout = static_cast<const uint16_t*>(a.x) + t * a.ld_x;
+  float dot[S];
+#pragma unroll
+  for (int j = 0; j < S; ++j) dot[j] = 0.f;
+  for (int c = threadIdx.x; c < a.nc; c += blockDim.x) {
+    Raw8<uint16_t> gr;
+    gr.load(dout + c * 8);
+    Raw8<Y> f[S];
+    if (a.y) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const int64_t p = __builtin_amdgcn_readlane(ch.row, lane[j]);
+        f[j].load(static_cast<const Y*>(a.y) + p * a.ld_y + c * 8);
+      }
+    }
+    float g[8];
+    gr.widen(g);
+    if (a.y) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        float v[8];
+        f[j].widen(v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dot[j] = __builtin_fmaf(g[k], v[k], dot[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      if (j >= n) break;
+      const int64_t p = __builtin_amdgcn_readlane(ch.row, lane[j]);
+      const float w = __uint_as_float(
+          (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(ch.weight), lane[j]));
+      float d[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[k] = w * g[k];
+      store8(static_cast<Y*>(a.out) + p * a.ld_out + c * 8, d);
+    }
+  }
+  if (!a.dweights) return;
+  const float s = wave_sums<S>(dot);
+  const int l = threadIdx.x & 63;
+  __syncthreads();  // the sums of the choices before have been read
+  if (l % (64 / S) == 0) red[threadIdx.x >> 6][l / (64 / S)] = s;
+  __syncthreads();
+  if (threadIdx.x < n) {
+    float sum = red[0][threadIdx.x];
+    for (int k = 1; k < (int)(blockDim.x >> 6); ++k) sum += red[k][threadIdx.x];
+    int j = lane[0];
+#pragma unroll
+    for (int i = 1; i < S; ++i) j = threadIdx.x == i ? lane[i] : j;
+    a.dweights[t * a.top_k + j] = sum;
+  }
+}
+
+}  // namespace
+
+// y may be the output: a lane reads the values that it overwrites, and reads them first.
 template <typename Y>
 __global__ __launch_bounds__(256) void moe_combine_bwd_kernel(MoeArgs a) {
-  __shared__ float red[4][kAtOnce];
+  __shared__ float red[4][8];
   const int64_t t = blockIdx.x;
-  const uint16_t* dout = static_cast<const uint16_t*>(a.x) + t * a.ld_x;
-  const Y* y = static_cast<const Y*>(a.y);  // may be out: each value is read before it is written
-  Y* dy = static_cast<Y*>(a.out);
-  const int32_t* __restrict__ pos = a.pos + t * a.top_k;
-  const float* __restrict__ w = a.weights ? a.weights + t * a.top_k : nullptr;
-  const int waves = blockDim.x >> 6;
-  for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
-    float dot[kAtOnce];
-#pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) dot[j] = 0.f;
-    for (int c = threadIdx.x; c < a.nc; c += blockDim.x) {
-      float g[8];
-      load8(dout + c * 8, g);
-      float f[kAtOnce][8];
-      if (y) {
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int64_t p = j0 + j < a.top_k ? pos[j0 + j] : -1;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[j][k] = 0.f;
-          if (p >= 0 && p < a.R) load8(y + p * a.ld_y + c * 8, f[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) dot[j] = __builtin_fmaf(g[k], f[j][k], dot[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int64_t p = j0 + j < a.top_k ? pos[j0 + j] : -1;
-        if (p < 0 || p >= a.R) continue;
-        const float wj = w ? w[j0 + j] : 1.f;
-        float d[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = wj * g[k];
-        store8(dy + p * a.ld_out + c * 8, d);
-      }
-    }
-    if (!a.dweights) continue;
-#pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) dot[j] = wave_sum(dot[j]);
-    __syncthreads();  // the sums of the choices before have been read
-    if ((threadIdx.x & 63) == 0)
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) red[threadIdx.x >> 6][j] = dot[j];
-    __syncthreads();
-    const int j = threadIdx.x;
-    if (j < kAtOnce && j0 + j < a.top_k) {
-      float s = red[0][j];
-      for (int k = 1; k < waves; ++k) s += red[k][j];
-      const int64_t p = pos[j0 + j];
-      a.dweights[t * a.top_k + j0 + j] = p >= 0 && p < a.R ? s : 0.f;
-    }
+  Choices ch;
+  ch.read(a, t);
+  if (a.dweights && (int)threadIdx.x < a.top_k && !((ch.live >> threadIdx.x) & 1))
+    a.dweights[t * a.top_k + threadIdx.x] = 0.f;
+  for (uint64_t left = ch.live; left;) {
+    const int n = __popcll(left);
+    if (n > 4)
+      combine_bwd_step<8, Y>(a, ch, left, t, red);
+    else if (n > 2)
+      combine_bwd_step<4, Y>(a, ch, left, t, red);
+    else
+      combine_bwd_step<2, Y>(a, ch, left, t, red);
   }
 }
 
@@ -319,11 +462,19 @@ namespace {
 // Threads of a workgroup that owns one token: a lane per chunk, up to four waves.
 dim3 row_threads(int nc) { return dim3(nc >= 256 ? 256 : nc > 64 ? (nc + 63) / 64 * 64 : 64); }
 
+template <int CH>
+hipError_t run_dispatch(const MoeArgs& a, hipStream_t stream) {
+  const int64_t pieces = (a.nc + 64 * CH - 1) / (64 * CH);
+  hipLaunchKernelGGL(moe_dispatch_kernel<CH>, dim3((unsigned)((a.T * pieces + 3) / 4)), dim3(256),
+                     0, stream, a, (int)pieces);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_moe_dispatch(const MoeArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(moe_dispatch_kernel, dim3((unsigned)a.T), row_threads(a.nc), 0, stream, a);
-  return hipGetLastError();
+  const int64_t wide = (a.nc + 255) / 256;
+  return a.T * wide >= 2048 ? run_dispatch<4>(a, stream) : run_dispatch<1>(a, stream);
 }
 
 hipError_t launch_moe_combine(const MoeArgs& a, bool y_f32, bool out_f32, hipStream_t stream) {

@@ -123,7 +123,7 @@ size_t fp8rl_moe_sort_workspace_bytes(int64_t T, int32_t top_k, int32_t E);
  *   x   : bf16 [T][ld_x]          pos : [T][top_k] int32, its rows distinct (fp8rl_moe_sort's)
  *   out : bf16 [R][ld_out], not overlapping x
  * Requires N % 8 == 0, pitches multiples of 8 and >= N, 16-byte aligned rows, 1 <= top_k <= 64,
- * T < 2^24.
+ * T < 2^24, T * ceil(N / 2048) < 2^26.
  */
 fp8rl_status fp8rl_moe_dispatch(const uint16_t* x, int64_t ld_x, const int32_t* pos, int64_t T,
                                 int32_t top_k, int64_t N, uint16_t* out, int64_t R, int64_t ld_out,
@@ -208,7 +208,7 @@ typedef struct {
  * by piece).
  * bf16 q_out may be written in place of q.
  * Requires head_dim % 8 == 0, 8 <= head_dim <= 512, rot_dim % 16 == 0, kv_heads >= 1,
- * page_size >= 1, num_pages * page_size < 2^62, T * (q_heads + 2 kv_heads) < 2^26, eps finite and
+ * page_size >= 1, num_pages * page_size < 2^62, T * (q_heads + 2 kv_heads) < 2^25, eps finite and
  * > 0 where norms are given; bf16 pointers 16-byte and codes 8-byte aligned, the table 16-byte,
  * pitches and strides multiples of 8 elements, ld_* >= the columns, page_stride (with more than
  * one page), slot_stride and head_stride >= head_dim. A NaN stores a NaN code. T == 0 returns FP8RL_OK.

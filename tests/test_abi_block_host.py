@@ -52,6 +52,10 @@ def test_header_is_strict_c99_and_its_struct_is_the_bindings(tmp_path):
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
     assert got == [ctypes.sizeof(_block.RopeKvArgs)] + [getattr(_block.RopeKvArgs, n).offset
                                                         for n in fields]
+    # the bytes that the binding packs are that struct too
+    values = [0.5 if n == "eps" else i + 1 for i, n in enumerate(fields)]
+    packed = _block.RopeKvArgs.from_buffer_copy(_block._pack_rope(*values))
+    assert [getattr(packed, n) for n in fields] == values
 
 
 def test_norm_refusals(L):
@@ -165,6 +169,7 @@ def test_row_refusals(L):
     assert call(k=0) == EARG
     assert call(k=65) == EARG
     assert call(T=1 << 24) == ESHAPE
+    assert call(T=1 << 20, N=1 << 17, ldx=1 << 17, ldo=1 << 17) == ESHAPE  # 2^26 waves
 
     base2 = dict(y=A, yt=0, R=8, ldy=64, pos=A, w=A, T=4, k=2, N=64, out=A, ot=0, ldo=64)
 
