@@ -49,37 +49,43 @@ __device__ __forceinline__ uint32_t amax8_bits(const float (&f)[8]) {
   return m;
 }
 
-// Sum of a row's partial sums over the W waves that share it.
-template <int W>
+// Sum over the lanes that share a row: L of them inside a wave, or (L == 0) the whole workgroup.
+template <int L, int W>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-  v = wave_sum(v);
-  if (W == 1) return v;
+#pragma unroll
+  for (int o = L ? L / 2 : 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if (L) return v;
+  const int waves = W ? W : (int)(blockDim.x >> 6);
+  if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   v = red[0];
-#pragma unroll
-  for (int k = 1; k < W; ++k) v += red[k];
+  for (int k = 1; k < waves; ++k) v += red[k];
   return v;
 }
 
 }  // namespace
 
-// W waves share a row (W == 1: a workgroup of 4 waves takes 4 rows), each lane holding CH chunks of
-// 8 values in registers: one read of x, residual and w, no second pass over memory. Lane l of the
-// row's 64 W takes chunks l, l + 64 W, ...: a group of 128 values is 16 neighbouring lanes.
-template <int W, int CH>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void add_rmsnorm_quant_kernel(NormArgs a) {
-  __shared__ float red[W];
-  const int lane = W == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-  if (W == 1 && row >= a.M) return;  // whole waves; W == 1 has no barrier
+// A row is held in registers, CH chunks of 8 values per lane: one read of x, residual and w, no
+// second pass over memory. It is shared by L lanes of a wave (L < 64: a wave takes 64 / L rows, a
+// workgroup of 256 threads 256 / L), or with L == 0 by a whole workgroup of as many waves as it
+// needs. Lane l of a row's n lanes takes chunks l, l + n, ...: a group of 128 values is 16
+// neighbouring lanes.
+template <int CH, int L, int W>
+__global__ __launch_bounds__(L ? 256 : W ? 64 * W : 1024) void add_rmsnorm_quant_kernel(NormArgs a) {
+  __shared__ float red[16];
+  const int step = L ? L : W ? 64 * W : (int)blockDim.x;
+  const int lane = (int)threadIdx.x % step;
+  const int64_t row = L ? (int64_t)blockIdx.x * (256 / (L ? L : 1)) + threadIdx.x / step
+                        : (int64_t)blockIdx.x;
+  if (L && row >= a.M) return;  // all lanes of a row; no barrier follows
   const u32x4* x = reinterpret_cast<const u32x4*>(a.x + row * a.ld_x);
   const u32x4* __restrict__ wt = reinterpret_cast<const u32x4*>(a.weight);
 
   u32x4 hv[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = lane + 64 * W * i;
+    const int c = lane + step * i;
     hv[i] = u32x4{0u, 0u, 0u, 0u};
     if (c < a.nc) hv[i] = __builtin_nontemporal_load(x + c);
   }
@@ -88,14 +94,14 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void add_rmsnorm_quant_kerne
     u32x4 rv[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = lane + 64 * W * i;
+      const int c = lane + step * i;
       rv[i] = u32x4{0u, 0u, 0u, 0u};
       if (c < a.nc) rv[i] = __builtin_nontemporal_load(res + c);
     }
     u32x4* h = reinterpret_cast<u32x4*>(a.h + row * a.ld_h);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = lane + 64 * W * i;
+      const int c = lane + step * i;
       float f[8], g[8];
       widen8(hv[i], f);
       widen8(rv[i], g);
@@ -110,7 +116,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void add_rmsnorm_quant_kerne
   float amax[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = lane + 64 * W * i;
+    const int c = lane + step * i;
     float f[8], g[8];
     widen8(hv[i], f);
 #pragma unroll
@@ -128,13 +134,13 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void add_rmsnorm_quant_kerne
       }
     }
   }
-  const float r = row_rstd(row_sum<W>(ss, red), 0.125f / (float)a.nc, a.eps);
+  const float r = row_rstd(row_sum<L, W>(ss, red), 0.125f / (float)a.nc, a.eps);
 
   if (a.xq) {
     float* sa = a.sa + row * (a.nc >> 4);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = lane + 64 * W * i;
+      const int c = lane + step * i;
       if (c >= a.nc) continue;
       float S = amax[i] == 0.f ? (r == r ? 1.f : r) : div448((double)amax[i] * (double)r);
       if (a.pow2) {
@@ -154,7 +160,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void add_rmsnorm_quant_kerne
     u32x4* y = reinterpret_cast<u32x4*>(a.y + row * a.ld_y);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = lane + 64 * W * i;
+      const int c = lane + step * i;
       if (c >= a.nc) continue;
       float f[8], g[8];
       widen8(hv[i], f);
@@ -173,16 +179,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void add_rmsnorm_quant_kerne
 namespace {
 
 // The chunks of one row that a thread holds: dy, h and, where there is one, dh.
-template <int CH, int STEP>
+template <int CH>
 struct BwdRow {
   u32x4 g[CH], h[CH], s[CH];
-  __device__ __forceinline__ void load(const NormBwdArgs& a, int64_t row, int c0) {
+  __device__ __forceinline__ void load(const NormBwdArgs& a, int64_t row, int c0, int step) {
     const u32x4* dy = reinterpret_cast<const u32x4*>(a.dy + row * a.ld_dy);
     const u32x4* hp = reinterpret_cast<const u32x4*>(a.h + row * a.ld_h);
     const u32x4* dh = reinterpret_cast<const u32x4*>(a.dh + row * a.ld_dh);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = c0 + STEP * i;
+      const int c = c0 + step * i;
       g[i] = h[i] = s[i] = u32x4{0u, 0u, 0u, 0u};
       if (c < a.nc) {
         g[i] = __builtin_nontemporal_load(dy + c);
@@ -192,7 +198,7 @@ struct BwdRow {
     if (a.dh) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = c0 + STEP * i;
+        const int c = c0 + step * i;
         if (c < a.nc) s[i] = __builtin_nontemporal_load(dh + c);
       }
     }
@@ -212,7 +218,7 @@ struct BwdRow {
       }
     }
   }
-  __device__ __forceinline__ void finish(const NormBwdArgs& a, int64_t row, int c0,
+  __device__ __forceinline__ void finish(const NormBwdArgs& a, int64_t row, int c0, int step,
                                          u32x4 (&wt)[CH], float r, float lean,
                                          float (&acc)[CH][8]) {
     u32x4* dx = reinterpret_cast<u32x4*>(a.dx + row * a.ld_dx);
@@ -221,7 +227,7 @@ struct BwdRow {
       // widened again from the 16-byte chunks: kept from sums(), the float32 values would take
       // twice the registers of what was loaded all through the reduction
       asm volatile("" : "+v"(h[i]), "+v"(g[i]), "+v"(wt[i]));
-      const int c = c0 + STEP * i;
+      const int c = c0 + step * i;
       float f[8], d[8], w[8], o[8];
       widen8(h[i], f);
       widen8(g[i], d);
@@ -237,21 +243,23 @@ struct BwdRow {
   }
 };
 
-template <int CH, int STEP>
-__device__ __forceinline__ void load_weights(const NormBwdArgs& a, int c0, u32x4 (&wt)[CH]) {
+template <int CH>
+__device__ __forceinline__ void load_weights(const NormBwdArgs& a, int c0, int step,
+                                             u32x4 (&wt)[CH]) {
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = c0 + STEP * i;
+    const int c = c0 + step * i;
     wt[i] = c < a.nc ? reinterpret_cast<const u32x4*>(a.weight)[c] : u32x4{0u, 0u, 0u, 0u};
   }
 }
 
-template <int CH, int STEP>
-__device__ __forceinline__ void store_part(const NormBwdArgs& a, int c0, const float (&acc)[CH][8]) {
+template <int CH>
+__device__ __forceinline__ void store_part(const NormBwdArgs& a, int c0, int step,
+                                           const float (&acc)[CH][8]) {
   float4* part = reinterpret_cast<float4*>(a.part) + (int64_t)blockIdx.x * (2 * a.nc);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = c0 + STEP * i;
+    const int c = c0 + step * i;
     if (c >= a.nc) continue;
     part[2 * c] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     part[2 * c + 1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
@@ -260,32 +268,44 @@ __device__ __forceinline__ void store_part(const NormBwdArgs& a, int c0, const f
 
 }  // namespace
 
-// Rows of up to 64 CH chunks: each of a workgroup's RW waves takes whole rows, with no barrier
-// between them; the waves' shares of dw are added through LDS at the end, in a fixed order.
-template <int RW, int CH>
+// Rows of up to 64 CH chunks: L lanes of a wave take a whole row (64 / L rows a wave), with no
+// barrier between the RW waves of a workgroup; the rows' shares of dw are added across the wave and
+// then through LDS at the end, in a fixed order.
+template <int RW, int CH, int L>
 __global__ __launch_bounds__(64 * RW, 2) void add_rmsnorm_bwd_wave_kernel(NormBwdArgs a) {
-  __shared__ float red[RW / 2][CH * 8][64];
-  const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+  __shared__ float red[RW / 2][CH * 8][L];
+  const int lane = (int)threadIdx.x % L, wave = (int)(threadIdx.x >> 6);
   const float inv_k = 0.125f / (float)a.nc;
   u32x4 wt[CH];
-  load_weights<CH, 64>(a, lane, wt);
+  load_weights<CH>(a, lane, L, wt);
   float acc[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
 
-  for (int64_t row = (int64_t)blockIdx.x * RW + wave; row < a.M; row += (int64_t)gridDim.x * RW) {
-    BwdRow<CH, 64> v;
-    v.load(a, row, lane);
+  constexpr int kRows = RW * 64 / L;  // of a workgroup's pass
+  for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / L; row < a.M;
+       row += (int64_t)gridDim.x * kRows) {
+    BwdRow<CH> v;
+    v.load(a, row, lane, L);
     float ss, sd;
     v.sums(wt, ss, sd);
-    ss = wave_sum(ss);
-    sd = wave_sum(sd);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) {
+      ss += __shfl_xor(ss, o, 64);
+      sd += __shfl_xor(sd, o, 64);
+    }
     const float r = row_rstd(ss, inv_k, a.eps);
-    v.finish(a, row, lane, wt, r, r * r * (sd * inv_k), acc);
+    v.finish(a, row, lane, L, wt, r, r * r * (sd * inv_k), acc);
   }
   if (!a.part) return;
+#pragma unroll
+  for (int o = L; o < 64; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[i][k] += __shfl_xor(acc[i][k], o, 64);
 #pragma unroll
   for (int n = RW / 2; n > 0; n >>= 1) {
     if (wave >= n && wave < 2 * n)
@@ -301,17 +321,18 @@ __global__ __launch_bounds__(64 * RW, 2) void add_rmsnorm_bwd_wave_kernel(NormBw
         for (int k = 0; k < 8; ++k) acc[i][k] += red[wave][8 * i + k][lane];
     __syncthreads();
   }
-  if (wave == 0) store_part<CH, 64>(a, lane, acc);
+  if (threadIdx.x < L) store_part<CH>(a, lane, L, acc);
 }
 
-// Wider rows: a workgroup of W waves takes a row, the next row's loads in flight while it reduces.
-template <int W, int CH, bool AHEAD>
-__global__ __launch_bounds__(64 * W) void add_rmsnorm_bwd_kernel(NormBwdArgs a) {
-  __shared__ float red[2][2][W];
-  const int t = (int)threadIdx.x;
+// A workgroup of as many waves as a row needs takes a row at a time; AHEAD: the next row's loads are
+// in flight while it reduces.
+template <int CH, bool AHEAD>
+__global__ __launch_bounds__(1024) void add_rmsnorm_bwd_kernel(NormBwdArgs a) {
+  __shared__ float red[2][2][16];
+  const int t = (int)threadIdx.x, step = (int)blockDim.x, waves = step >> 6;
   const float inv_k = 0.125f / (float)a.nc;
   u32x4 wt[CH];
-  load_weights<CH, 64 * W>(a, t, wt);
+  load_weights<CH>(a, t, step, wt);
   float acc[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
@@ -319,15 +340,15 @@ __global__ __launch_bounds__(64 * W) void add_rmsnorm_bwd_kernel(NormBwdArgs a) 
     for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
 
   int buf = 0;
-  BwdRow<CH, 64 * W> v;
+  BwdRow<CH> v;
   int64_t row = blockIdx.x;
-  if (AHEAD && row < a.M) v.load(a, row, t);
+  if (AHEAD && row < a.M) v.load(a, row, t, step);
   for (; row < a.M; row += gridDim.x, buf ^= 1) {
     // in place of dy or dh: the next row's values are read before this row's are written, and no
     // other workgroup writes them
-    BwdRow<CH, 64 * W> next;
-    if (!AHEAD) v.load(a, row, t);
-    if (AHEAD && row + gridDim.x < a.M) next.load(a, row + gridDim.x, t);
+    BwdRow<CH> next;
+    if (!AHEAD) v.load(a, row, t, step);
+    if (AHEAD && row + gridDim.x < a.M) next.load(a, row + gridDim.x, t, step);
     float ss, sd;
     v.sums(wt, ss, sd);
     ss = wave_sum(ss);
@@ -337,13 +358,12 @@ __global__ __launch_bounds__(64 * W) void add_rmsnorm_bwd_kernel(NormBwdArgs a) 
     if ((t & 63) == 0) red[buf][0][t >> 6] = ss, red[buf][1][t >> 6] = sd;
     __syncthreads();
     ss = red[buf][0][0], sd = red[buf][1][0];
-#pragma unroll
-    for (int k = 1; k < W; ++k) ss += red[buf][0][k], sd += red[buf][1][k];
+    for (int k = 1; k < waves; ++k) ss += red[buf][0][k], sd += red[buf][1][k];
     const float r = row_rstd(ss, inv_k, a.eps);
-    v.finish(a, row, t, wt, r, r * r * (sd * inv_k), acc);
+    v.finish(a, row, t, step, wt, r, r * r * (sd * inv_k), acc);
     if (AHEAD) v = next;
   }
-  if (a.part) store_part<CH, 64 * W>(a, t, acc);
+  if (a.part) store_part<CH>(a, t, step, acc);
 }
 
 // dw[k] = sum over the groups of their partial sums: 8 columns of 4 values per workgroup, 32
@@ -372,57 +392,87 @@ __global__ __launch_bounds__(256) void norm_dw_kernel(const float4* __restrict__
 
 namespace {
 
-template <int W, int CH>
-hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
-  const int64_t wgs = W == 1 ? (a.M + 3) / 4 : a.M;
-  hipLaunchKernelGGL((add_rmsnorm_quant_kernel<W, CH>), dim3((unsigned)wgs),
-                     dim3(W == 1 ? 256 : 64 * W), 0, stream, a);
-  return hipGetLastError();
+// L lanes per row, or a workgroup of the waves that nc chunks need at CH a lane.
+template <int CH, int L, int W = 0>
+void run_norm(const NormArgs& a, hipStream_t stream) {
+  const int64_t rows = L ? 256 / (L ? L : 1) : 1;
+  const int threads = L ? 256 : 64 * ((a.nc + 64 * CH - 1) / (64 * CH));
+  hipLaunchKernelGGL((add_rmsnorm_quant_kernel<CH, L, W>), dim3((unsigned)((a.M + rows - 1) / rows)),
+                     dim3(threads), 0, stream, a);
 }
 
 }  // namespace
 
+// Which lanes share a row. Up to 64 chunks (K <= 512) a wave or a part of one: at K = 128 and 262144
+// rows 47 us against 298 us with a workgroup per row. Up to 256 chunks (K <= 2048) a wave per row
+// when there are 8192 rows or more: 42.8 against 46.6 us (K = 1024, 32768 rows) and 45.4 against
+// 54.3 us (K = 1152), but 6.4 against 5.2 us at 2048 rows of K = 1024, where a quarter of the waves
+// is too few to hide the loads. Wider rows by about four waves, 2 to 4 chunks a lane; up to 512 rows
+// (two a CU) by one chunk a lane, up to 16 waves: 4.0 against 4.8 us (64 rows, K = 4096), 4.7
+// against 6.1 us (K = 8192). Four waves have a form with their number known (its sums unrolled):
+// 42.2 against 43.8 us at 8192 x 4096, 235.9 MB, 5.6 TB/s: what a copy of this size reaches here
+// (5.2 - 5.5 TB/s), so memory bounds it.
 hipError_t launch_add_rmsnorm_quant(const NormArgs& a, hipStream_t stream) {
-  const int nc = a.nc;
-  if (nc <= 256) return run_norm<4, 1>(a, stream);
-  if (nc <= 512) return run_norm<4, 2>(a, stream);
-  if (nc <= 1024) return run_norm<4, 4>(a, stream);
-  if (nc <= 2048) return run_norm<16, 2>(a, stream);
-  return run_norm<16, 4>(a, stream);
+  const bool few = a.M <= 512, many = a.M >= 8192;
+  if (a.nc <= 16) run_norm<1, 16>(a, stream);
+  else if (a.nc <= 32) run_norm<1, 32>(a, stream);
+  else if (a.nc <= 64) run_norm<1, 64>(a, stream);
+  else if (many && a.nc <= 128) run_norm<2, 64>(a, stream);
+  else if (many && a.nc <= 192) run_norm<3, 64>(a, stream);
+  else if (many && a.nc <= 256) run_norm<4, 64>(a, stream);
+  else if (!few && a.nc > 192 && a.nc <= 256) run_norm<1, 0, 4>(a, stream);
+  else if (!few && a.nc > 384 && a.nc <= 512) run_norm<2, 0, 4>(a, stream);
+  else if (a.nc <= (few ? 1024 : 256)) run_norm<1, 0>(a, stream);
+  else if (a.nc <= (few ? 2048 : 512)) run_norm<2, 0>(a, stream);
+  else if (!few && a.nc <= 768) run_norm<3, 0>(a, stream);
+  else run_norm<4, 0>(a, stream);
+  return hipGetLastError();
 }
 
 namespace {
 
-// How the backward pass of M rows of nc chunks is cut up: waves per row-taking unit and groups.
+// How the backward pass of M rows of nc chunks is cut up. A wave per row up to 256 chunks (K <= 2048)
+// once there are more than 512 rows (27.4 us at 8192 x 2048, 5.1 TB/s; 7.9 us by workgroups against
+// 8.6 us by waves at 512 rows, 12.5 against 8.9 us at 1024); wider rows by a workgroup each (49.8
+// against 55.3 us at 8192 x 4096, where a wave would hold 256 registers). Every workgroup leaves K
+// partial sums: 512 of them keep all CUs busy twice (49.8 us; 256: 60 us at 4096 x 8192 against 56,
+// 1024: 56 us at 8192 x 4096), 256 are enough up to 1024 rows (10.0 against 12.1 us at 512 x 4096).
 struct BwdShape {
-  bool wave_rows;  // a wave per row (rows of up to 512 chunks), else a workgroup
-  int rw;          // waves of a workgroup that take rows of their own
-  int64_t groups;
+  int lanes;       // of a wave that share a row; 0: a workgroup takes a row
+  int rw;          // lanes > 0: waves of a workgroup
+  int ch;          // chunks of a lane
+  int64_t groups;  // workgroups
 };
 BwdShape bwd_shape(int64_t M, int64_t nc) {
-  if (nc <= 512) {
-    const int rw = M >= 8 * 256 ? 8 : 4;
-    const int64_t most = 256 * (8 / rw), g = (M + rw - 1) / rw;
-    return {true, rw, g < most ? g : most};
+  if (nc <= 64 || (nc <= 256 && M > 512)) {
+    const int lanes = nc <= 16 ? 16 : nc <= 32 ? 32 : 64;
+    const int ch = nc <= 64 ? 1 : nc <= 128 ? 2 : 4;
+    const int rw = M * lanes >= 8 * 256 * 64 ? 8 : 4;
+    const int64_t most = 256 * (8 / rw), rows = rw * 64 / lanes, g = (M + rows - 1) / rows;
+    return {lanes, rw, ch, g < most ? g : most};
   }
-  return {false, 1, M < 512 ? M : 512};
+  const int ch = M <= 512 && nc <= 1024 ? 1 : nc <= 2048 ? 2 : 4;
+  const int64_t most = M > 1024 && nc <= 1024 ? 512 : 256;
+  return {0, 0, ch, M < most ? M : most};
 }
 
-template <int RW, int CH>
+template <int RW, int CH, int L>
 void run_bwd_wave(const NormBwdArgs& a, int64_t groups, hipStream_t stream) {
-  hipLaunchKernelGGL((add_rmsnorm_bwd_wave_kernel<RW, CH>), dim3((unsigned)groups), dim3(64 * RW),
-                     0, stream, a);
+  hipLaunchKernelGGL((add_rmsnorm_bwd_wave_kernel<RW, CH, L>), dim3((unsigned)groups),
+                     dim3(64 * RW), 0, stream, a);
 }
 template <int RW>
-void run_bwd_waves(const NormBwdArgs& a, int64_t groups, hipStream_t stream) {
-  if (a.nc <= 64) run_bwd_wave<RW, 1>(a, groups, stream);
-  else if (a.nc <= 128) run_bwd_wave<RW, 2>(a, groups, stream);
-  else if (a.nc <= 256) run_bwd_wave<RW, 4>(a, groups, stream);
-  else run_bwd_wave<RW, 8>(a, groups, stream);
+void run_bwd_waves(const NormBwdArgs& a, const BwdShape& s, hipStream_t stream) {
+  if (s.lanes == 16) run_bwd_wave<RW, 1, 16>(a, s.groups, stream);
+  else if (s.lanes == 32) run_bwd_wave<RW, 1, 32>(a, s.groups, stream);
+  else if (s.ch == 1) run_bwd_wave<RW, 1, 64>(a, s.groups, stream);
+  else if (s.ch == 2) run_bwd_wave<RW, 2, 64>(a, s.groups, stream);
+  else run_bwd_wave<RW, 4, 64>(a, s.groups, stream);
 }
-template <int W, int CH, bool AHEAD>
+template <int CH, bool AHEAD>
 void run_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t stream) {
-  hipLaunchKernelGGL((add_rmsnorm_bwd_kernel<W, CH, AHEAD>), dim3((unsigned)groups), dim3(64 * W), 0,
+  const int threads = 64 * ((a.nc + 64 * CH - 1) / (64 * CH));
+  hipLaunchKernelGGL((add_rmsnorm_bwd_kernel<CH, AHEAD>), dim3((unsigned)groups), dim3(threads), 0,
                      stream, a);
 }
 
@@ -433,11 +483,11 @@ int64_t norm_bwd_groups(int64_t M, int64_t K) { return bwd_shape(M, K / 8).group
 hipError_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dw, hipStream_t stream) {
   const BwdShape s = bwd_shape(a.M, a.nc);
   if (s.groups > 0) {
-    if (s.wave_rows && s.rw == 8) run_bwd_waves<8>(a, s.groups, stream);
-    else if (s.wave_rows) run_bwd_waves<4>(a, s.groups, stream);
-    else if (a.nc <= 1024) run_bwd<8, 2, true>(a, s.groups, stream);
-    else if (a.nc <= 2048) run_bwd<16, 2, true>(a, s.groups, stream);
-    else run_bwd<16, 4, false>(a, s.groups, stream);
+    if (s.lanes && s.rw == 8) run_bwd_waves<8>(a, s, stream);
+    else if (s.lanes) run_bwd_waves<4>(a, s, stream);
+    else if (s.ch == 1) run_bwd<1, true>(a, s.groups, stream);
+    else if (s.ch == 2) run_bwd<2, true>(a, s.groups, stream);
+    else run_bwd<4, false>(a, s.groups, stream);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   if (!dw) return hipSuccess;
