@@ -1,5 +1,6 @@
 // C ABI entry points of the operators between the linears: argument validation (host only, before
 // any HIP call) and dispatch.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -31,7 +32,8 @@ fp8rl_status check_norm_shape(int64_t M, int64_t K) {
   return FP8RL_OK;
 }
 
-bool bad_eps(float eps) { return !(eps > 0.f) || isinf(eps); }
+// (a smaller eps beside a row of zeros has no finite reciprocal root in float32)
+bool bad_eps(float eps) { return !(eps >= FLT_MIN) || isinf(eps); }
 
 }  // namespace
 

@@ -73,6 +73,8 @@ hipError_t launch_rope_kv_append(const fp8rl_rope_kv_args& a, hipStream_t stream
 // Device helpers
 // ---------------------------------------------------------------------------------------------
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 // The 8 bf16 values of a 16-byte chunk as float32 (exact).
 __device__ __forceinline__ void widen8(u32x4 w, float (&f)[8]) {
   f[0] = bf16_lo(w.x), f[1] = bf16_hi(w.x), f[2] = bf16_lo(w.y), f[3] = bf16_hi(w.y);

@@ -217,8 +217,6 @@ hipError_t launch_moe_sort(const void* ids, bool wide, int64_t n, int top_k, int
 // ---------------------------------------------------------------------------------------------
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 // 8 values as they lie in memory: what a load in flight occupies.
 template <typename T>
 struct Raw8;

@@ -366,26 +366,36 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_bwd_kernel(NormBwdArgs a) {
   if (a.part) store_part<CH>(a, t, step, acc);
 }
 
-// dw[k] = sum over the groups of their partial sums: 8 columns of 4 values per workgroup, 32
-// threads down each column, then their sums in order.
-__global__ __launch_bounds__(256) void norm_dw_kernel(const float4* __restrict__ part, int groups,
+// dw[k] = sum over the groups of their partial sums, in a fixed order: 8 columns of 4 values per
+// workgroup and 64 threads down each column with 8 loads in flight each, so that 512 groups are one
+// round of loads.
+__global__ __launch_bounds__(512) void norm_dw_kernel(const f32x4* __restrict__ part, int groups,
                                                       int nc4, float* __restrict__ dw) {
-  __shared__ float4 red[32][8];
+  __shared__ float red[8][32];
   const int col = threadIdx.x & 7, g0 = threadIdx.x >> 3;
-  const int c = blockIdx.x * 8 + col;  // K % 128 == 0: every column exists
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int g = g0; g < groups; g += 32) {
-    const float4 v = part[(int64_t)g * nc4 + c];
-    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  const f32x4* p = part + blockIdx.x * 8 + col;  // K % 128 == 0: every column exists
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  for (int g = g0; g < groups; g += 64 * 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (g + 64 * i < groups) v[i] = p[(int64_t)(g + 64 * i) * nc4];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += v[i];
   }
-  red[g0][col] = s;
+#pragma unroll
+  for (int o = 8; o < 64; o <<= 1) {
+    s.x += __shfl_xor(s.x, o, 64), s.y += __shfl_xor(s.y, o, 64);
+    s.z += __shfl_xor(s.z, o, 64), s.w += __shfl_xor(s.w, o, 64);
+  }
+  if ((threadIdx.x & 63) < 8) *reinterpret_cast<f32x4*>(&red[threadIdx.x >> 6][4 * col]) = s;
   __syncthreads();
   if (threadIdx.x < 32) {
-    const float* r = reinterpret_cast<const float*>(red) + threadIdx.x;
-    float sum = r[0];
+    float sum = red[0][threadIdx.x];
 #pragma unroll
-    for (int k = 1; k < 32; ++k) sum += r[32 * k];
+    for (int k = 1; k < 8; ++k) sum += red[k][threadIdx.x];
     dw[blockIdx.x * 32 + threadIdx.x] = sum;
   }
 }
@@ -491,8 +501,8 @@ hipError_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dw, hipStream_t s
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   if (!dw) return hipSuccess;
-  hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)(a.nc / 4)), dim3(256), 0, stream,
-                     reinterpret_cast<const float4*>(a.part), (int)s.groups, 2 * a.nc, dw);
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)(a.nc / 4)), dim3(512), 0, stream,
+                     reinterpret_cast<const f32x4*>(a.part), (int)s.groups, 2 * a.nc, dw);
   return hipGetLastError();
 }
 

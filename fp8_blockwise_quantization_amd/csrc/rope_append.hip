@@ -24,14 +24,47 @@ struct RopeArgs {
   unsigned waves;  // T * per_token
   unsigned per_token;
   int64_t slots;   // num_pages * page_size
-  float inv_dim;   // 1 / head_dim
+  double inv_dim;  // 1 / head_dim
 };
 
-// (x, y) -> (x cos - y sin, y cos + x sin)
-__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
-  const float u = x, v = y;
-  x = __builtin_fmaf(u, c, -(v * s));
-  y = __builtin_fmaf(v, c, u * s);
+// A float64 on its way through float32 to a type of far fewer bits: cut off, and the last bit set
+// where something was (rounding to odd), so that the second rounding sees what the first dropped.
+__device__ __forceinline__ float narrow(double d) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, d);
+  const uint32_t lo = (uint32_t)u, rest = (lo & 0x1FFFFFFFu) + 0x1FFFFFFFu;  // bit 29: not all zero
+  const uint64_t odd = (u & 0xFFFFFFFF00000000u) | ((lo | rest) & 0xE0000000u);
+  return (float)__builtin_bit_cast(double, odd);
+}
+__device__ __forceinline__ float narrow(float f) { return f; }
+
+// (x, y) -> f (x cos - y sin, y cos + x sin), in the type of f.
+template <typename F>
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s, F f) {
+  const F u = (F)x, v = (F)y;
+  x = narrow(__builtin_elementwise_fma(u, (F)c, -(v * (F)s)) * f);
+  y = narrow(__builtin_elementwise_fma(v, (F)c, u * (F)s) * f);
+}
+
+// A lane's two chunks rotated where they are, and scaled by f. In float32 on the way to bf16. On the
+// way to E4M3 in float64, whose products here are exact: a code is a step of up to 1/8 of the value,
+// and float32's errors before it would put one value in a million on the wrong side of a step.
+// Unrotated columns and v go through float32 to the nearest, as the plain store's do.
+template <typename F>
+__device__ __forceinline__ void finish(float (&ua)[8], float (&ub)[8], const float (&c)[8],
+                                       const float (&s)[8], bool turned, bool halves, F f) {
+  if (!turned) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ua[k] = (float)((F)ua[k] * f), ub[k] = (float)((F)ub[k] * f);
+  } else if (halves) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) turn(ua[k], ub[k], c[k], s[k], f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      turn(ua[2 * k], ua[2 * k + 1], c[k], s[k], f);
+      turn(ub[2 * k], ub[2 * k + 1], c[4 + k], s[4 + k], f);
+    }
+  }
 }
 
 }  // namespace
@@ -112,40 +145,32 @@ __global__ __launch_bounds__(256) void rope_kv_append_kernel(RopeArgs args) {
     float ua[8], ub[8];
     widen8(va[i], ua);
     widen8(vb[i], ub);
+    double r = 1.0;
     if (kind < 2 && a.q_weight) {
       const u32x4* w = reinterpret_cast<const u32x4*>(kind == 0 ? a.q_weight : a.k_weight);
-      float wa[8], wb[8], ss = 0.f;
+      float wa[8], wb[8];
       widen8(has_a ? w[ca] : u32x4{0u, 0u, 0u, 0u}, wa);
       widen8(has_b ? w[cb] : u32x4{0u, 0u, 0u, 0u}, wb);
+      double ss = 0.0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        ss = __builtin_fmaf(ub[k], ub[k], __builtin_fmaf(ua[k], ua[k], ss));
+      for (int k = 0; k < 8; ++k) ss += (double)(ua[k] * ua[k]) + (double)(ub[k] * ub[k]);
 #pragma unroll
       for (int o = 1; o < G; o <<= 1) ss += __shfl_xor(ss, o, 64);
-      const float r = rsqrtf(ss * args.inv_dim + a.eps);
+      r = rsqrt(ss * args.inv_dim + (double)a.eps);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ua[k] = ua[k] * wa[k] * r, ub[k] = ub[k] * wb[k] * r;
-    }
-    if (kind < 2 && p < C) {
-      if (halves) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) turn(ua[k], ub[k], c[k], s[k]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          turn(ua[2 * k], ua[2 * k + 1], c[k], s[k]);
-          turn(ub[2 * k], ub[2 * k + 1], c[4 + k], s[4 + k]);
-        }
-      }
+      for (int k = 0; k < 8; ++k) ua[k] *= wa[k], ub[k] *= wb[k];  // exact: 8 + 8 bits
     }
     void* out = kind == 0 ? a.q_out : kind == 1 ? a.k_cache : a.v_cache;
     const int64_t dst = kind == 0 ? (int64_t)t * a.ld_qo + head * a.head_dim
                                   : cache_row + head * a.head_stride;
+    const bool turned = kind < 2 && p < C;
     if (kind == 0 ? a.q_scale : a.k_scale) {
+      finish(ua, ub, c, s, turned, halves, r * recip[kind]);
       u32x2* o = reinterpret_cast<u32x2*>(static_cast<uint8_t*>(out) + dst);
-      if (has_a) o[ca] = codes8(ua, recip[kind]);
-      if (has_b) o[cb] = codes8(ub, recip[kind]);
+      if (has_a) o[ca] = encode8(ua);
+      if (has_b) o[cb] = encode8(ub);
     } else {
+      finish(ua, ub, c, s, turned, halves, (float)r);
       u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + dst);
       if (has_a) o[ca] = round8(ua);
       if (has_b) o[cb] = round8(ub);
@@ -172,7 +197,7 @@ hipError_t launch_rope_kv_append(const fp8rl_rope_kv_args& a, hipStream_t stream
   RopeArgs r;
   r.a = a;
   r.slots = a.num_pages * (int64_t)a.page_size;
-  r.inv_dim = 1.f / (float)a.head_dim;
+  r.inv_dim = 1.0 / a.head_dim;
   const int heads = a.q_heads + 2 * a.kv_heads;
   const int chunks = a.head_dim / 8;
   int g = 1;

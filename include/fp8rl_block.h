@@ -16,6 +16,9 @@
  *   KV cache    q and k normalised per head where the model does that, rotated by their positions,
  *               k and v stored into a paged cache (fp8rl_rope_kv_append).
  *
+ * A workspace is overwritten and keeps nothing from one call for the next (no header to clear): any
+ * memory of the size will do, and calls may share it that do not run at the same time.
+ *
  * Where a result is said to be written "in place", the output may be the very memory (same pointer,
  * same pitch) of the named input; any other overlap of outputs with inputs is not allowed.
  */
@@ -44,7 +47,7 @@ extern "C" {
  *   x         : bf16, M rows of pitch ld_x (>= K)
  *   residual  : bf16, M rows of pitch ld_res, or NULL
  *   weight    : bf16, K values (dense)
- *   eps       : finite, > 0
+ *   eps       : finite, a normal positive float32 (at least 2^-126)
  *   h         : bf16 [M][ld_h], or NULL (not written). Needs a residual. May be written in place of
  *               x or of residual.
  *   y         : bf16 [M][ld_y], the normalised rows rounded once, or NULL. (The router of a
@@ -197,21 +200,23 @@ typedef struct {
  * token,
  *   u = x * weight / sqrt(mean(x^2) + eps)     (q and k, where q_weight and k_weight are given)
  *   w[a] = u[a] cos - u[b] sin,  w[b] = u[b] cos + u[a] sin     for every rotated pair (a, b)
- * in float32, rounded once, to bf16 or as fp8rl_quant_bf16_per_tensor to the E4M3 code of w / scale
+ * rounded once: to bf16 (formed in float32), or to the E4M3 code nearest to w / scale (formed in
+ * float64; columns that are not rotated, and v, as fp8rl_quant_bf16_per_tensor rounds them)
  * (saturating). q goes to q_out, k (and v, neither normalised nor rotated) to row
  *   cache + page * page_stride + place * slot_stride + head * head_stride,
  *   page = slot / page_size, place = slot % page_size,
  * so pages may be laid out token by token, head by head, or with keys and values interleaved. A
  * token whose slot is negative or past the last page stores nothing; one whose position lies
- * outside [0, max_pos) (with rot_dim > 0) is skipped altogether, q included. Every byte that no token names is
- * left as it was. Slots must be distinct (of two tokens with one slot, either may be kept, piece
- * by piece).
+ * outside [0, max_pos) (with rot_dim > 0) is skipped altogether, q included. Every byte that no
+ * token names is left as it was. Slots must be distinct (of two tokens with one slot, either may be
+ * kept, piece by piece).
  * bf16 q_out may be written in place of q.
  * Requires head_dim % 8 == 0, 8 <= head_dim <= 512, rot_dim % 16 == 0, kv_heads >= 1,
- * page_size >= 1, num_pages * page_size < 2^62, T * (q_heads + 2 kv_heads) < 2^25, eps finite and
- * > 0 where norms are given; bf16 pointers 16-byte and codes 8-byte aligned, the table 16-byte,
- * pitches and strides multiples of 8 elements, ld_* >= the columns, page_stride (with more than
- * one page), slot_stride and head_stride >= head_dim. A NaN stores a NaN code. T == 0 returns FP8RL_OK.
+ * page_size >= 1, num_pages * page_size < 2^62, T * (q_heads + 2 kv_heads) < 2^25, eps as for
+ * fp8rl_add_rmsnorm_quant where norms are given; bf16 pointers 16-byte and codes 8-byte aligned,
+ * the table 16-byte, pitches and strides multiples of 8 elements, ld_* >= the columns, page_stride
+ * (with more than one page), slot_stride and head_stride >= head_dim. A NaN stores a NaN code.
+ * T == 0 returns FP8RL_OK.
  */
 fp8rl_status fp8rl_rope_kv_append(const fp8rl_rope_kv_args* args, void* stream);
 

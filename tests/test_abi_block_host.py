@@ -74,7 +74,7 @@ def test_norm_refusals(L):
     assert call(sa=None) == ENULL
     assert call(xq=None, sa=None, y=None) == ENULL  # nothing to write
     assert call(res=None) == EARG  # h without a residual
-    for eps in (0.0, -1e-6, NAN, INF):
+    for eps in (0.0, -1e-6, NAN, INF, 1e-39):
         assert call(eps=eps) == EARG, eps
     assert call(fmt=2) == EARG
     assert call(M=-1) == ESHAPE

@@ -171,6 +171,24 @@ def test_append_without_q_and_padded_rows():
     check(c, skipped=(2, 7))
 
 
+@pytest.mark.parametrize("norms", [False, True])
+def test_codes_are_correctly_rounded(norms):
+    """The codes of q and k are those of the float64 values: no value lands on the wrong side of a
+    step (none of these lies within float64's error of one)."""
+    c = Case(700, 8, 4, 128, 128, norms=norms, q8=True, seed=13, spare=9)
+    c.slots = torch.arange(700, device="cuda")
+    q = c.call()
+    torch.cuda.synchronize()
+    for got, x, w, s in ((q.view(700, 8, 128), c.q, c.qw, c.qs),
+                         (c.kc.reshape(-1, 4, 128)[:700], c.k, c.kw, c.ks)):
+        v = np.clip(c.turned(x, w)[0] / np.float64(float(s)), -448, 448)
+        step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6))) - 3)
+        want = np.clip(np.rint(v / step) * step, -448, 448)
+        # v is off by float64's roundings (and so may sit on the other side within 2^-45 of a tie)
+        tie = np.abs(np.abs(v / step - np.floor(v / step)) - 0.5) < 2.0 ** -40
+        assert np.array_equal(e4m3.decode(got.cpu().numpy())[~tie], want[~tie])
+
+
 def test_append_q_in_place_equals_out_of_place():
     for norms in (False, True):
         c = Case(37, 8, 2, 128, 96, norms=norms, seed=6)

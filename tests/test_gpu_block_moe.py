@@ -195,6 +195,30 @@ def test_rows_past_the_end_are_left_out():
     assert dw[0, 1] == 0 and dw[1, 1] == 0 and bool((dw[3] == 0).all()) and dw[2, 0] == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_what_no_choice_names_does_not_matter(dtype):
+    """NaN and infinities in grouped rows that no choice names, and in the weights of choices without
+    a row, reach nothing."""
+    T, k, E, N = 70, 11, 6, 136
+    pos, R = layout(T, k, E, 21)
+    g = torch.Generator().manual_seed(22)
+    y = torch.randn((R + 9, N), generator=g).to(dtype).cuda()
+    w = torch.rand((T, k), generator=g).cuda()
+    dout = torch.randn((T, N), generator=g).to(torch.bfloat16).cuda()
+    named = torch.zeros(R + 9, dtype=torch.bool, device="cuda")
+    named[pos[pos >= 0].long()] = True
+    assert not bool(named.all()) and bool((pos < 0).any())
+    y2, w2 = y.clone(), w.clone()
+    y2[~named] = float("nan")
+    y2[R + 3] = float("inf")
+    w2[pos < 0] = float("nan")
+    dy = torch.zeros_like(y)
+    for a, b in ((fq.moe_combine(y, pos, weights=w), fq.moe_combine(y2, pos, weights=w2)),
+                 *zip(fq.moe_combine_bwd(dout, y, pos, weights=w, dy=dy.clone()),
+                      fq.moe_combine_bwd(dout, y2, pos, weights=w2, dy=dy.clone()))):
+        assert torch.equal(a, b) and bool(torch.isfinite(b).all())
+
+
 def test_no_tokens_no_rows():
     e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
     pos0 = torch.empty((0, 2), dtype=torch.int32, device="cuda")
