@@ -15,7 +15,7 @@ import struct
 import torch
 
 from . import _lib
-from ._lib import FP8RL_OUT_BF16, FP8RL_OUT_F32, _check, _on_stream, _scale_code
+from ._lib import FP8RL_OUT_BF16, FP8RL_OUT_F32, FP8RL_SCALE_FP32, _check, _on_stream, _scale_code
 
 FP8RL_IDS_I32 = 0
 FP8RL_IDS_I64 = 1
@@ -166,13 +166,15 @@ def _flat(t, name, dtype, n, dev):
     _fail(name, t, dtype, (n,), dev)
 
 
-def _workspace(workspace, need, dev):
-    """(tensor to keep alive, address, bytes) of a call's workspace, allocated if none is given."""
+def _workspace(workspace, need, t, dev):
+    """(tensor to keep alive, address, bytes) of a call's workspace, allocated beside t if none is
+    given."""
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        workspace = t.new_empty(need, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), need
+    if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -205,7 +207,8 @@ def fp8rl_add_rmsnorm_quant(x, weight, residual=None, eps=1e-6, h=None, y=None, 
     dev = _here(x, stream)
     if dev < 0:
         with _at(x, "x", stream):
-            return fp8rl_add_rmsnorm_quant(x, weight, residual, eps, h, y, xq, sa, rows, codes, scale)
+            return fp8rl_add_rmsnorm_quant(x, weight, residual, eps, h, y, xq, sa, rows, codes,
+                                           scale)
     bf16 = torch.bfloat16
     M, K = _is_2d(x, "x")
     px, ld_x = _matrix(x, "x", bf16, (M, K), dev)
@@ -229,9 +232,10 @@ def fp8rl_add_rmsnorm_quant(x, weight, residual=None, eps=1e-6, h=None, y=None, 
             sa = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
         pq, ld_q = _matrix(xq, "xq", torch.uint8, (M, K), dev)
         ps = _vector(sa, "sa", torch.float32, (M, K // 128), dev)
+    fmt = FP8RL_SCALE_FP32 if scale == "fp32" else _scale_code(scale)
     _check(_block_lib().fp8rl_add_rmsnorm_quant(px, ld_x, pr, ld_r, pw, eps, M, K, ph, ld_h, py,
-                                                ld_y, pq, ld_q, ps, 0 if scale == "fp32" else _scale_code(scale),
-                                                _raw_stream(dev)), "fp8rl_add_rmsnorm_quant")
+                                                ld_y, pq, ld_q, ps, fmt, _raw_stream(dev)),
+           "fp8rl_add_rmsnorm_quant")
     return xq, sa, h, y
 
 
@@ -263,7 +267,7 @@ def fp8rl_add_rmsnorm_bwd(dy, h, weight, dh=None, eps=1e-6, dx=None, dw=None,
     po = _flat(dw, "dw", torch.float32, K, dev) if dw is not None else None
     L = _block_lib()
     need = L.fp8rl_add_rmsnorm_bwd_workspace_bytes(M, K) if dw is not None else 0
-    keep, ws, nbytes = _workspace(workspace, need, dev)
+    keep, ws, nbytes = _workspace(workspace, need, dy, dev)
     _check(L.fp8rl_add_rmsnorm_bwd(pg, ld_g, ph, ld_h, pw, pd, ld_d, eps, M, K, px, ld_x, po, ws,
                                    nbytes, _raw_stream(dev)), "fp8rl_add_rmsnorm_bwd")
     return dx, dw
@@ -301,7 +305,8 @@ def fp8rl_moe_sort(topk_ids, E: int, expert_offsets=None, row_ids=None, pos=None
     pr = _flat(row_ids, "row_ids", i32, T * k, dev)
     pp = _vector(pos, "pos", i32, (T, k), dev)
     L = _block_lib()
-    keep, ws, nbytes = _workspace(workspace, L.fp8rl_moe_sort_workspace_bytes(T, k, E), dev)
+    keep, ws, nbytes = _workspace(workspace, L.fp8rl_moe_sort_workspace_bytes(T, k, E), topk_ids,
+                                  dev)
     wide = FP8RL_IDS_I64 if topk_ids.dtype == torch.int64 else FP8RL_IDS_I32
     _check(L.fp8rl_moe_sort(pi, wide, T, k, E, po, pr, pp, ws, nbytes, _raw_stream(dev)),
            "fp8rl_moe_sort")

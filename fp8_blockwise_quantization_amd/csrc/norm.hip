@@ -324,8 +324,9 @@ __global__ __launch_bounds__(64 * RW, 2) void add_rmsnorm_bwd_wave_kernel(NormBw
   if (threadIdx.x < L) store_part<CH>(a, lane, L, acc);
 }
 
-// A workgroup of as many waves as a row needs takes a row at a time; AHEAD: the next row's loads are
-// in flight while it reduces.
+// A workgroup of as many waves as a row needs takes a row at a time; AHEAD: the next row's loads
+// are in flight while it reduces (rows past K = 16384 would not fit the registers twice). 268 MB at
+// 8192 x 4096 in 50 us, 5.4 TB/s: what a copy of this size reaches.
 template <int CH, bool AHEAD>
 __global__ __launch_bounds__(1024) void add_rmsnorm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[2][2][16];
@@ -407,18 +408,18 @@ template <int CH, int L, int W = 0>
 void run_norm(const NormArgs& a, hipStream_t stream) {
   const int64_t rows = L ? 256 / (L ? L : 1) : 1;
   const int threads = L ? 256 : 64 * ((a.nc + 64 * CH - 1) / (64 * CH));
-  hipLaunchKernelGGL((add_rmsnorm_quant_kernel<CH, L, W>), dim3((unsigned)((a.M + rows - 1) / rows)),
-                     dim3(threads), 0, stream, a);
+  const dim3 grid((unsigned)((a.M + rows - 1) / rows));
+  hipLaunchKernelGGL((add_rmsnorm_quant_kernel<CH, L, W>), grid, dim3(threads), 0, stream, a);
 }
 
 }  // namespace
 
-// Which lanes share a row. Up to 64 chunks (K <= 512) a wave or a part of one: at K = 128 and 262144
-// rows 47 us against 298 us with a workgroup per row. Up to 256 chunks (K <= 2048) a wave per row
+// Which lanes share a row. Up to 64 chunks (K <= 512) a wave or a part of one: at K = 128 and
+// 262144 rows 47 us against 298 us with a workgroup per row. Up to 256 chunks (K <= 2048) a wave per row
 // when there are 8192 rows or more: 42.8 against 46.6 us (K = 1024, 32768 rows) and 45.4 against
 // 54.3 us (K = 1152), but 6.4 against 5.2 us at 2048 rows of K = 1024, where a quarter of the waves
-// is too few to hide the loads. Wider rows by about four waves, 2 to 4 chunks a lane; up to 512 rows
-// (two a CU) by one chunk a lane, up to 16 waves: 4.0 against 4.8 us (64 rows, K = 4096), 4.7
+// is too few to hide the loads. Wider rows by about four waves, 2 to 4 chunks a lane; up to 512
+// rows (two a CU) by one chunk a lane, up to 16 waves: 4.0 against 4.8 us (64 rows, K = 4096), 4.7
 // against 6.1 us (K = 8192). Four waves have a form with their number known (its sums unrolled):
 // 42.2 against 43.8 us at 8192 x 4096, 235.9 MB, 5.6 TB/s: what a copy of this size reaches here
 // (5.2 - 5.5 TB/s), so memory bounds it.
@@ -441,8 +442,8 @@ hipError_t launch_add_rmsnorm_quant(const NormArgs& a, hipStream_t stream) {
 
 namespace {
 
-// How the backward pass of M rows of nc chunks is cut up. A wave per row up to 256 chunks (K <= 2048)
-// once there are more than 512 rows (27.4 us at 8192 x 2048, 5.1 TB/s; 7.9 us by workgroups against
+// How the backward pass of M rows of nc chunks is cut up. A wave per row up to 256 chunks
+// (K <= 2048) once there are more than 512 rows (27.4 us at 8192 x 2048, 5.1 TB/s; 7.9 us by workgroups against
 // 8.6 us by waves at 512 rows, 12.5 against 8.9 us at 1024); wider rows by a workgroup each (49.8
 // against 55.3 us at 8192 x 4096, where a wave would hold 256 registers). Every workgroup leaves K
 // partial sums: 512 of them keep all CUs busy twice (49.8 us; 256: 60 us at 4096 x 8192 against 56,

@@ -12,7 +12,10 @@
 //
 // A wave takes U * 64 / G heads of one token: what belongs to the token (its position, slot, page
 // and row addresses) is scalar, its cosines and sines are fetched once, and the heads' rows are in
-// flight together.
+// flight together. Two heads a lane group in large calls (36 us at 8192 tokens of 48 heads of 128
+// with E4M3 outputs, 155 MB, one: 43 us, three: 36 us but 39 against 37 us with bf16 outputs), one
+// where that leaves CUs idle. With bf16 outputs memory bounds it (206 MB in 37.4 us, 5.5 TB/s),
+// with E4M3 ones the conversions take about as long as the bytes (16384 tokens: 63 us, 4.9 TB/s).
 #include "block_ops.hpp"
 
 namespace fp8rl {

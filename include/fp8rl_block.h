@@ -78,7 +78,8 @@ fp8rl_status fp8rl_add_rmsnorm_quant(const uint16_t* x, int64_t ld_x, const uint
  *   dw            : float32, K values, overwritten (zeros when M == 0), or NULL (not computed)
  *   workspace     : at least fp8rl_add_rmsnorm_bwd_workspace_bytes(M, K) bytes, 16-byte aligned,
  *                   overwritten; may be NULL when dw is
- * Requires K % 128 == 0, K <= 32768, M < 2^22; alignment as for fp8rl_add_rmsnorm_quant (dw 4-byte).
+ * Requires K % 128 == 0, K <= 32768, M < 2^22; alignment as for fp8rl_add_rmsnorm_quant (dw
+ * 4-byte).
  * Deterministic: the sum over rows has a fixed order.
  */
 fp8rl_status fp8rl_add_rmsnorm_bwd(const uint16_t* dy, int64_t ld_dy, const uint16_t* h,
