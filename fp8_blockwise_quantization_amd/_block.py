@@ -1,21 +1,23 @@
-"""ctypes binding of the operators between the FP8 linears (include/fp8rl_block.h).
+"""Python face of the operators between the FP8 linears (include/fp8rl_block.h).
 
 As in ``_lib``: argument marshalling only, one Python function per C entry point, outputs allocated
 where the caller gives none, a non-zero status raised as ``Fp8rlError``. The tensors of a call must
 live on one device, which need not be the current one; the call runs there on that device's current
 stream, or on ``stream``.
+
+The checks of a call's tensors are compiled (``_marshal``, csrc/marshal.cpp): interpreted, they took
+longer than the launch they precede (an append's 22 tensors 8 us, a norm's seven 3 us).
 """
 
 from __future__ import annotations
 
 import contextlib
 import ctypes
-import struct
 
 import torch
 
 from . import _lib
-from ._lib import FP8RL_OUT_BF16, FP8RL_OUT_F32, FP8RL_SCALE_FP32, _check, _on_stream, _scale_code
+from ._lib import FP8RL_SCALE_FP32, _check, _on_stream, _scale_code
 
 FP8RL_IDS_I32 = 0
 FP8RL_IDS_I64 = 1
@@ -70,7 +72,7 @@ def declare_block(L: ctypes.CDLL) -> ctypes.CDLL:
         "fp8rl_moe_combine": (ci, [vp, ci, i64, i64, vp, vp, i64, i32, i64, vp, ci, i64, vp]),
         "fp8rl_moe_combine_bwd": (ci, [vp, i64, vp, i64, ci, i64, vp, vp, i64, i32, i64, vp, i64,
                                        vp, vp]),
-        "fp8rl_rope_kv_append": (ci, [vp, vp]),  # the struct by reference or as its bytes
+        "fp8rl_rope_kv_append": (ci, [ctypes.POINTER(RopeKvArgs), vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -78,10 +80,6 @@ def declare_block(L: ctypes.CDLL) -> ctypes.CDLL:
         f.argtypes = args
     return L
 
-
-# RopeKvArgs as struct.pack lays it out (native alignment, like the C struct): filling bytes costs a
-# fraction of filling a ctypes structure.
-_pack_rope = struct.Struct("@PPPqqqqiiiiifPPqPPPqPPPPPPqiqqq").pack
 
 _L = None
 
@@ -93,7 +91,21 @@ def _block_lib() -> ctypes.CDLL:
     return _L
 
 
-_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_m = None
+
+
+def _marshal():
+    """The compiled marshalling module, loaded once."""
+    global _m
+    if _m is None:
+        _lib.lib()  # raises where nothing is built
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise RuntimeError("the argument marshalling is not built: run "
+                               "`python -m fp8_blockwise_quantization_amd.build`") from e
+        _m = module
+    return _m
 
 
 @contextlib.contextmanager
@@ -112,82 +124,14 @@ def _here(t, stream) -> int:
     """The device of a call's first tensor where the call can run as things stand; else -1 (a
     stream was given, or the device is not the current one, or t is no device tensor)."""
     dev = t.get_device() if isinstance(t, torch.Tensor) else -1
-    return dev if stream is None and dev >= 0 and dev == _device() else -1
+    return dev if stream is None and dev >= 0 and dev == torch._C._cuda_getDevice() else -1
 
 
 # The address of the device's current stream in torch (`stream` itself under _at).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _fail(name, t, dtype, shape, dev):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a device (cuda) tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call runs on cuda:{dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be dense along its last dimension (and contiguous where it is "
-                     "no matrix of rows)")
-
-
-def _matrix(t, name, dtype, shape, dev):
-    """(address, row pitch) of a [rows][cols] matrix with unit column stride."""
-    try:
-        stride = t.stride()
-        if (t.dtype is dtype and t.get_device() == dev and t.shape == shape
-                and (stride[1] == 1 or shape[1] <= 1)):
-            return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
-    except AttributeError:  # no tensor
-        pass
-    _fail(name, t, dtype, shape, dev)
-
-
-def _vector(t, name, dtype, shape, dev):
-    """Address of a contiguous tensor."""
-    try:
-        if (t.dtype is dtype and t.get_device() == dev and t.shape == shape
-                and t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _fail(name, t, dtype, shape, dev)
-
-
-def _flat(t, name, dtype, n, dev):
-    """Address of a contiguous tensor of n values."""
-    try:
-        if (t.dtype is dtype and t.get_device() == dev and t.numel() == n
-                and t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _fail(name, t, dtype, (n,), dev)
-
-
-def _workspace(workspace, need, t, dev):
-    """(tensor to keep alive, address, bytes) of a call's workspace, allocated beside t if none is
-    given."""
-    if workspace is None:
-        if need == 0:
-            return None, None, 0
-        workspace = t.new_empty(need, dtype=torch.uint8)
-        return workspace, workspace.data_ptr(), need
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _out_type(t, name):
-    if t.dtype == torch.bfloat16:
-        return FP8RL_OUT_BF16
-    if t.dtype == torch.float32:
-        return FP8RL_OUT_F32
-    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-
-
-def _is_2d(t, name):
+def _shape2(t, name):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     return t.shape
@@ -209,33 +153,20 @@ def fp8rl_add_rmsnorm_quant(x, weight, residual=None, eps=1e-6, h=None, y=None, 
         with _at(x, "x", stream):
             return fp8rl_add_rmsnorm_quant(x, weight, residual, eps, h, y, xq, sa, rows, codes,
                                            scale)
-    bf16 = torch.bfloat16
-    M, K = _is_2d(x, "x")
-    px, ld_x = _matrix(x, "x", bf16, (M, K), dev)
-    pw = _flat(weight, "weight", bf16, K, dev)
-    pr = ph = py = pq = ps = None
-    ld_r = ld_h = ld_y = ld_q = 0
-    if residual is not None:
-        pr, ld_r = _matrix(residual, "residual", bf16, (M, K), dev)
-        if h is None:
-            h = torch.empty((M, K), dtype=bf16, device=x.device)
-    if h is not None:
-        ph, ld_h = _matrix(h, "h", bf16, (M, K), dev)
+    if residual is not None and h is None:
+        h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
     if rows and y is None:
-        y = torch.empty((M, K), dtype=bf16, device=x.device)
-    if y is not None:
-        py, ld_y = _matrix(y, "y", bf16, (M, K), dev)
-    if codes or xq is not None or sa is not None:
-        if xq is None:
-            xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-        if sa is None:
-            sa = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
-        pq, ld_q = _matrix(xq, "xq", torch.uint8, (M, K), dev)
-        ps = _vector(sa, "sa", torch.float32, (M, K // 128), dev)
+        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    if xq is None or sa is None:
+        if codes or xq is not None or sa is not None:
+            M, K = _shape2(x, "x")
+            if xq is None:
+                xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+            if sa is None:
+                sa = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
     fmt = FP8RL_SCALE_FP32 if scale == "fp32" else _scale_code(scale)
-    _check(_block_lib().fp8rl_add_rmsnorm_quant(px, ld_x, pr, ld_r, pw, eps, M, K, ph, ld_h, py,
-                                                ld_y, pq, ld_q, ps, fmt, _raw_stream(dev)),
-           "fp8rl_add_rmsnorm_quant")
+    _check((_m or _marshal()).add_rmsnorm_quant(x, weight, residual, eps, h, y, xq, sa, fmt, dev,
+                                                _raw_stream(dev)), "fp8rl_add_rmsnorm_quant")
     return xq, sa, h, y
 
 
@@ -253,23 +184,12 @@ def fp8rl_add_rmsnorm_bwd(dy, h, weight, dh=None, eps=1e-6, dx=None, dw=None,
     if dev < 0:
         with _at(dy, "dy", stream):
             return fp8rl_add_rmsnorm_bwd(dy, h, weight, dh, eps, dx, dw, weight_grad, workspace)
-    bf16 = torch.bfloat16
-    M, K = _is_2d(dy, "dy")
-    pg, ld_g = _matrix(dy, "dy", bf16, (M, K), dev)
-    ph, ld_h = _matrix(h, "h", bf16, (M, K), dev)
-    pw = _flat(weight, "weight", bf16, K, dev)
-    pd, ld_d = _matrix(dh, "dh", bf16, (M, K), dev) if dh is not None else (None, 0)
     if dx is None:
-        dx = torch.empty((M, K), dtype=bf16, device=dy.device)
-    px, ld_x = _matrix(dx, "dx", bf16, (M, K), dev)
+        dx = torch.empty(dy.shape, dtype=torch.bfloat16, device=dy.device)
     if dw is None and weight_grad:
-        dw = torch.empty(K, dtype=torch.float32, device=dy.device)
-    po = _flat(dw, "dw", torch.float32, K, dev) if dw is not None else None
-    L = _block_lib()
-    need = L.fp8rl_add_rmsnorm_bwd_workspace_bytes(M, K) if dw is not None else 0
-    keep, ws, nbytes = _workspace(workspace, need, dy, dev)
-    _check(L.fp8rl_add_rmsnorm_bwd(pg, ld_g, ph, ld_h, pw, pd, ld_d, eps, M, K, px, ld_x, po, ws,
-                                   nbytes, _raw_stream(dev)), "fp8rl_add_rmsnorm_bwd")
+        dw = torch.empty(_shape2(dy, "dy")[1], dtype=torch.float32, device=dy.device)
+    _check((_m or _marshal()).add_rmsnorm_bwd(dy, h, weight, dh, eps, dx, dw, workspace, dev,
+                                              _raw_stream(dev)), "fp8rl_add_rmsnorm_bwd")
     return dx, dw
 
 
@@ -290,26 +210,14 @@ def fp8rl_moe_sort(topk_ids, E: int, expert_offsets=None, row_ids=None, pos=None
     if dev < 0:
         with _at(topk_ids, "topk_ids", stream):
             return fp8rl_moe_sort(topk_ids, E, expert_offsets, row_ids, pos, workspace)
-    T, k = _is_2d(topk_ids, "topk_ids")
-    if topk_ids.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"topk_ids must be torch.int32 or torch.int64, got {topk_ids.dtype}")
-    i32, device = torch.int32, topk_ids.device
-    pi = _vector(topk_ids, "topk_ids", topk_ids.dtype, (T, k), dev)
     if expert_offsets is None:
-        expert_offsets = torch.empty(E + 1, dtype=i32, device=device)
+        expert_offsets = torch.empty(max(E, 0) + 1, dtype=torch.int32, device=topk_ids.device)
     if row_ids is None:
-        row_ids = torch.empty(T * k, dtype=i32, device=device)
+        row_ids = torch.empty(topk_ids.numel(), dtype=torch.int32, device=topk_ids.device)
     if pos is None:
-        pos = torch.empty((T, k), dtype=i32, device=device)
-    po = _flat(expert_offsets, "expert_offsets", i32, E + 1, dev)
-    pr = _flat(row_ids, "row_ids", i32, T * k, dev)
-    pp = _vector(pos, "pos", i32, (T, k), dev)
-    L = _block_lib()
-    keep, ws, nbytes = _workspace(workspace, L.fp8rl_moe_sort_workspace_bytes(T, k, E), topk_ids,
-                                  dev)
-    wide = FP8RL_IDS_I64 if topk_ids.dtype == torch.int64 else FP8RL_IDS_I32
-    _check(L.fp8rl_moe_sort(pi, wide, T, k, E, po, pr, pp, ws, nbytes, _raw_stream(dev)),
-           "fp8rl_moe_sort")
+        pos = torch.empty(topk_ids.shape, dtype=torch.int32, device=topk_ids.device)
+    _check((_m or _marshal()).moe_sort(topk_ids, E, expert_offsets, row_ids, pos, workspace, dev,
+                                       _raw_stream(dev)), "fp8rl_moe_sort")
     return expert_offsets, row_ids, pos
 
 
@@ -320,15 +228,9 @@ def fp8rl_moe_dispatch(x, pos, out=None, stream=None):
     if dev < 0:
         with _at(x, "x", stream):
             return fp8rl_moe_dispatch(x, pos, out)
-    T, N = _is_2d(x, "x")
-    k = _is_2d(pos, "pos")[1]
-    px, ld_x = _matrix(x, "x", torch.bfloat16, (T, N), dev)
-    pp = _vector(pos, "pos", torch.int32, (T, k), dev)
     if out is None:
-        out = torch.empty((T * k, N), dtype=torch.bfloat16, device=x.device)
-    R = _is_2d(out, "out")[0]
-    po, ld_o = _matrix(out, "out", torch.bfloat16, (R, N), dev)
-    _check(_block_lib().fp8rl_moe_dispatch(px, ld_x, pp, T, k, N, po, R, ld_o, _raw_stream(dev)),
+        out = torch.empty((pos.numel(), _shape2(x, "x")[1]), dtype=torch.bfloat16, device=x.device)
+    _check((_m or _marshal()).moe_dispatch(x, pos, out, dev, _raw_stream(dev)),
            "fp8rl_moe_dispatch")
     return out
 
@@ -340,18 +242,11 @@ def fp8rl_moe_combine(y, pos, weights=None, out_dtype=torch.bfloat16, out=None, 
     if dev < 0:
         with _at(y, "y", stream):
             return fp8rl_moe_combine(y, pos, weights, out_dtype, out)
-    R, N = _is_2d(y, "y")
-    T, k = _is_2d(pos, "pos")
-    kind = _out_type(y, "y")
-    py, ld_y = _matrix(y, "y", y.dtype, (R, N), dev)
-    pp = _vector(pos, "pos", torch.int32, (T, k), dev)
-    pw = _vector(weights, "weights", torch.float32, (T, k), dev) if weights is not None else None
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=y.device)
-    out_kind = _out_type(out, "out")
-    po, ld_o = _matrix(out, "out", out.dtype, (T, N), dev)
-    _check(_block_lib().fp8rl_moe_combine(py, kind, R, ld_y, pp, pw, T, k, N, po, out_kind, ld_o,
-                                          _raw_stream(dev)), "fp8rl_moe_combine")
+        out = torch.empty((_shape2(pos, "pos")[0], _shape2(y, "y")[1]), dtype=out_dtype,
+                          device=y.device)
+    _check((_m or _marshal()).moe_combine(y, pos, weights, out, dev, _raw_stream(dev)),
+           "fp8rl_moe_combine")
     return out
 
 
@@ -365,47 +260,22 @@ def fp8rl_moe_combine_bwd(dout, y, pos, weights=None, dy=None, dweights=None, R=
     if dev < 0:
         with _at(dout, "dout", stream):
             return fp8rl_moe_combine_bwd(dout, y, pos, weights, dy, dweights, R, y_dtype)
-    T, N = _is_2d(dout, "dout")
-    k = _is_2d(pos, "pos")[1]
-    pg, ld_g = _matrix(dout, "dout", torch.bfloat16, (T, N), dev)
-    pp = _vector(pos, "pos", torch.int32, (T, k), dev)
-    pw = _vector(weights, "weights", torch.float32, (T, k), dev) if weights is not None else None
-    py = pd = None
-    ld_y = 0
     if y is not None:
-        R, y_dtype = _is_2d(y, "y")[0], y.dtype
-        py, ld_y = _matrix(y, "y", y_dtype, (R, N), dev)
         if dweights is None:
-            dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device)
-        pd = _vector(dweights, "dweights", torch.float32, (T, k), dev)
+            dweights = torch.empty(pos.shape, dtype=torch.float32, device=dout.device)
+        if dy is None:
+            dy = torch.empty(y.shape, dtype=y.dtype, device=dout.device)
     elif dweights is not None:
         raise ValueError("dweights needs y")
-    if dy is None:
-        dy = torch.empty((T * k if R is None else R, N), dtype=y_dtype, device=dout.device)
-    elif y is None:
-        R, y_dtype = _is_2d(dy, "dy")[0], dy.dtype
-    R = dy.shape[0] if R is None else R
-    kind = _out_type(dy, "dy")
-    po, ld_o = _matrix(dy, "dy", y_dtype, (R, N), dev)
-    _check(_block_lib().fp8rl_moe_combine_bwd(pg, ld_g, py, ld_y, kind, R, pp, pw, T, k, N, po,
-                                              ld_o, pd, _raw_stream(dev)), "fp8rl_moe_combine_bwd")
+    elif dy is None:
+        dy = torch.empty((pos.numel() if R is None else R, _shape2(dout, "dout")[1]),
+                         dtype=y_dtype, device=dout.device)
+    _check((_m or _marshal()).moe_combine_bwd(dout, y, pos, weights, dy, dweights, dev,
+                                              _raw_stream(dev)), "fp8rl_moe_combine_bwd")
     return dy, dweights
 
 
 # -------------------------------------------------------------------------------------- KV cache
-
-
-def _cache(t, name, dtype, shape, strides, dev):
-    """Address of a cache view of the first one's shape and strides."""
-    try:
-        if (t.dtype is dtype and t.get_device() == dev and t.shape == shape
-                and (strides[3] == 1 or shape[3] <= 1)):
-            if t.stride() != strides and shape[0] > 0:
-                raise ValueError("k_cache and v_cache must have the same strides")
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _fail(name, t, dtype, shape, dev)
 
 
 def fp8rl_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out=None,
@@ -427,50 +297,10 @@ def fp8rl_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_c
             return fp8rl_rope_kv_append(
                 q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, interleaved,
                 q_weight, k_weight, eps, q_scale, k_scale, v_scale)
-    bf16 = torch.bfloat16
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be 4-D: [page][place][head][column]")
-    pages, page, Hkv, D = k_cache.shape
-    T = _is_2d(k, "k")[0]
-    pk, ld_k = _matrix(k, "k", bf16, (T, Hkv * D), dev)
-    pv, ld_v = _matrix(v, "v", bf16, (T, Hkv * D), dev)
-    kind = bf16 if k_scale is None else torch.uint8
-    strides = k_cache.stride()
-    pkc = _cache(k_cache, "k_cache", kind, k_cache.shape, strides, dev)
-    pvc = _cache(v_cache, "v_cache", kind, k_cache.shape, strides, dev)
-    # a dimension of one entry has no stride to speak of
-    page_stride = strides[0] if pages > 1 else 0
-    slot_stride = strides[1] if page > 1 else D
-    head_stride = strides[2] if Hkv > 1 else D
-    pq = po = ld_q = ld_o = Hq = 0
-    if q is not None:
-        cols = _is_2d(q, "q")[1]
-        if D == 0 or cols % D:
-            raise ValueError(f"q has {cols} columns, no multiple of the head width {D}")
-        Hq = cols // D
-        pq, ld_q = _matrix(q, "q", bf16, (T, cols), dev)
-        q_kind = bf16 if q_scale is None else torch.uint8
-        if q_out is None:
-            q_out = torch.empty((T, cols), dtype=q_kind, device=k.device)
-        po, ld_o = _matrix(q_out, "q_out", q_kind, (T, cols), dev)
-    rot = max_pos = pc = pp = qw = kw = qs = ks = vs = 0
-    if cos_sin is not None:
-        max_pos, rot = _is_2d(cos_sin, "cos_sin")
-        pc = _vector(cos_sin, "cos_sin", torch.float32, (max_pos, rot), dev)
-        pp = _flat(positions, "positions", torch.int64, T, dev)
-    ps = _flat(slot_mapping, "slot_mapping", torch.int64, T, dev)
-    if q_weight is not None:
-        qw = _flat(q_weight, "q_weight", bf16, D, dev)
-    if k_weight is not None:
-        kw = _flat(k_weight, "k_weight", bf16, D, dev)
-    if q_scale is not None:
-        qs = _flat(q_scale, "q_scale", torch.float32, 1, dev)
-    if k_scale is not None:
-        ks = _flat(k_scale, "k_scale", torch.float32, 1, dev)
-    if v_scale is not None:
-        vs = _flat(v_scale, "v_scale", torch.float32, 1, dev)
-    args = _pack_rope(pq, pk, pv, ld_q, ld_k, ld_v, T, Hq, Hkv, D, rot, 1 if interleaved else 0,
-                      eps, pp, pc, max_pos, qw, kw, po, ld_o, qs, ps, pkc, pvc, ks, vs, pages,
-                      page, page_stride, slot_stride, head_stride)
-    _check(_block_lib().fp8rl_rope_kv_append(args, _raw_stream(dev)), "fp8rl_rope_kv_append")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16 if q_scale is None else torch.uint8,
+                            device=k.device)
+    _check((_m or _marshal()).rope_kv_append(
+        q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, interleaved, q_weight,
+        k_weight, eps, q_scale, k_scale, v_scale, dev, _raw_stream(dev)), "fp8rl_rope_kv_append")
     return q_out

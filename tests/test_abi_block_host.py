@@ -52,10 +52,6 @@ def test_header_is_strict_c99_and_its_struct_is_the_bindings(tmp_path):
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
     assert got == [ctypes.sizeof(_block.RopeKvArgs)] + [getattr(_block.RopeKvArgs, n).offset
                                                         for n in fields]
-    # the bytes that the binding packs are that struct too
-    values = [0.5 if n == "eps" else i + 1 for i, n in enumerate(fields)]
-    packed = _block.RopeKvArgs.from_buffer_copy(_block._pack_rope(*values))
-    assert [getattr(packed, n) for n in fields] == values
 
 
 def test_norm_refusals(L):
@@ -257,6 +253,24 @@ def test_append_refusals(L):
     assert call(num_pages=1 << 60) == ESHAPE
     assert call(max_pos=-1) == ESHAPE
     assert call(max_pos=1 << 31) == ESHAPE
+
+
+def test_marshalling_module_refuses_before_any_launch():
+    """The compiled checks by themselves: argument counts, types, tensors that are none or not on
+    the device."""
+    m = _block._marshal()
+    x, w = torch.zeros((2, 128), dtype=torch.bfloat16), torch.zeros(128, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        m.add_rmsnorm_quant(x, w)
+    with pytest.raises(ValueError, match="x must be a device"):
+        m.add_rmsnorm_quant(x, w, None, 1e-6, None, None, None, None, 0, 0, 0)
+    with pytest.raises(ValueError, match="topk_ids must be a device"):
+        m.moe_sort([1, 2], 4, None, None, None, None, 0, 0)
+    with pytest.raises(TypeError):
+        m.moe_combine(x, w, None, x, "0", 0)
+    with pytest.raises(ValueError, match="k must be a device"):
+        m.rope_kv_append(None, x, x, None, None, None, None, None, None, False, None, None, 1e-6,
+                         None, None, None, 0, 0)
 
 
 def test_python_binding_refuses_host_tensors():
