@@ -185,7 +185,7 @@ typedef struct {
   const uint16_t* k_weight;
   void* q_out;          /* [T][ld_qo]: bf16, or E4M3 codes where q_scale is given */
   int64_t ld_qo;
-  const float* q_scale; /* one float32 (device), or NULL */
+  const float* q_scale; /* one float32 (device; positive, finite), or NULL */
   const int64_t* slot_mapping; /* [T]: page * page_size + place in the page; negative: no store */
   void* k_cache;        /* bf16, or E4M3 codes where k_scale and v_scale are given */
   void* v_cache;

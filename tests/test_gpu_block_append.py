@@ -134,6 +134,17 @@ def test_append_shapes(T, Hq, Hkv, D, rot, norms):
     check(Case(T, Hq, Hkv, D, rot, norms=norms, seed=T + D))
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,more", [
+    (9001, 24, 4, 16, 16, dict(norms=True)), (4500, 26, 3, 32, 16, dict(q8=True, pairs=True)),
+    (2000, 32, 4, 64, 64, dict(heads_first=True, norms=True, q8=True)),
+    (1003, 20, 4, 96, 96, dict(cache8=False)), (1000, 14, 2, 256, 128, dict(q8=True, norms=True)),
+    (301, 24, 3, 512, 512, dict(cache8=False, pairs=True))])
+def test_append_of_many_tokens(T, Hq, Hkv, D, rot, more):
+    """Enough tokens for two heads a lane, at every number of lanes that share a head."""
+    print(f"[append] T={T} {Hq}/{Hkv} x {D} rot={rot} {more}", flush=True)
+    check(Case(T, Hq, Hkv, D, rot, seed=T, **more))
+
+
 @pytest.mark.parametrize("cache8,q8", [(True, True), (True, False), (False, False), (False, True)])
 @pytest.mark.parametrize("heads_first", [False, True])
 @pytest.mark.parametrize("pairs", [False, True])

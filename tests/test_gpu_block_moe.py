@@ -120,6 +120,24 @@ def test_dispatch(T, k, E, N):
     assert torch.equal(buf, want) and out.data_ptr() == buf[:, 8:].data_ptr()
 
 
+@pytest.mark.parametrize("T,k,N", [(2100, 3, 136), (700, 5, 4104), (2048, 2, 2048), (2500, 1, 64)])
+@pytest.mark.parametrize("lines", [True, False])
+def test_dispatch_of_many_tokens(T, k, N, lines):
+    """Rows that start on 128-byte lines and rows that do not, four chunks a lane."""
+    print(f"[dispatch] T={T} k={k} N={N} lines={lines}", flush=True)
+    pos, R = layout(T, k, 16, 33)
+    x = synth.act_bf16(T, N, seed=34).cuda()
+    pitch = -(-N // 64) * 64 + (0 if lines else 8)
+    buf = torch.full((R, pitch), 3.0, dtype=torch.bfloat16, device="cuda")
+    fq.moe_dispatch(x, pos, out=buf[:, :N])
+    torch.cuda.synchronize()
+    want = torch.full_like(buf, 3.0)
+    p = pos.long().view(-1)
+    token = torch.arange(T, device="cuda").repeat_interleave(k)
+    want[p[p >= 0], :N] = x[token[p >= 0]]
+    assert torch.equal(buf, want)
+
+
 @pytest.mark.parametrize("y_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,k,E,N", SHAPES)

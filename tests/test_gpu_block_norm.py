@@ -58,8 +58,10 @@ def check_norm(x, res, w, eps, out, what):
         assert_within(f64(sa), S, R * S, what + " scales")
 
 
-# one row up to many, one group up to the widest row, chunks that do not fill the threads
-SHAPES = [(1, 128), (1, 2048), (3, 4096), (64, 4096), (5, 384), (130, 2176), (33, 5120), (7, 8192),
+# one row up to many, one group up to the widest row, chunks that do not fill the threads; with the
+# row counts at which lanes are dealt out differently
+SHAPES = [(8193, 1024), (8200, 1152), (8192, 2048), (600, 2176), (530, 5120), (2100, 512),
+          (8200, 128), (4100, 256), (700, 1024), (1, 128), (1, 2048), (3, 4096), (64, 4096), (5, 384), (130, 2176), (33, 5120), (7, 8192),
           (9, 11008), (4, 16384), (3, 20480), (2, 32768), (1500, 2048), (2111, 4096), (4099, 1152),
           (1100, 7168)]
 
