@@ -179,7 +179,8 @@ __global__ __launch_bounds__(1024) void moe_place_kernel(const ID* __restrict__ 
       at = __shfl(at, __ffsll((unsigned long long)same) - 1, 64) + below;
       if (i < end) {
         pos[i] = e[j] < E ? at : -1;
-        if (e[j] < E) row_ids[at] = (int)((unsigned)i / (unsigned)top_k);
+        // (at < n but for ids that change while the call runs)
+        if (e[j] < E && at < n) row_ids[at] = (int)((unsigned)i / (unsigned)top_k);
       }
     }
   }

@@ -222,7 +222,7 @@ def test_norm_backward(M, K):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)  # the same bits
 
 
-@pytest.mark.parametrize("M,K", [(5, 256), (700, 2048)])
+@pytest.mark.parametrize("M,K", [(5, 256), (40, 4096), (700, 2048), (1500, 4224)])
 def test_norm_backward_in_place_and_pitches(M, K):
     g = torch.Generator().manual_seed(23)
     big = torch.randn((M, 3 * K + 8), generator=g).to(torch.bfloat16).cuda()
