@@ -128,7 +128,7 @@ def _here(t, stream) -> int:
 
 
 # The address of the device's current stream in torch (`stream` itself under _at).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (none without a GPU build)
 
 
 def _shape2(t, name):

@@ -56,7 +56,7 @@ def build_marshal(verbose: bool = False) -> str:
     returns the extension module's path."""
     import torch
 
-    cxx = shutil.which("g++") or shutil.which("c++")
+    cxx = shutil.which("g++") or shutil.which("c++") or shutil.which("clang++")
     if cxx is None:
         raise RuntimeError("a C++ compiler is required to build the argument marshalling")
     troot = os.path.dirname(torch.__file__)

@@ -253,6 +253,27 @@ def test_no_tokens_no_rows():
     assert dy.shape == (0, 64) and bool((dw == 0).all())
 
 
+def test_rows_past_32_bit_offsets():
+    """Grouped rows beyond 2^31 elements and 2^32 bytes of their buffer."""
+    N = 4096
+    R = (1 << 32) // (2 * N) + 70000
+    y = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
+    pos = torch.tensor([[0, R - 1], [R - 40000, 7]], dtype=torch.int32, device="cuda")
+    x = synth.act_bf16(2, N, seed=41).cuda()
+    fq.moe_dispatch(x, pos, out=y)
+    assert torch.equal(y[pos.long()], x[:, None, :].expand(2, 2, N))
+    out = fq.moe_combine(y, pos, out_dtype=torch.float32)
+    assert torch.equal(out, 2 * x.float())
+    dout = synth.act_bf16(2, N, seed=42).cuda()
+    _, dw = fq.moe_combine_bwd(dout, y, pos, dy=y)
+    torch.cuda.synchronize()
+    assert torch.equal(y[pos.long()], dout[:, None, :].expand(2, 2, N))
+    want = (f64(dout) * f64(x)).sum(axis=1)
+    size = np.abs(f64(dout) * f64(x)).sum(axis=1)
+    assert_within(f64(dw), np.stack([want, want], 1), (N / 32 + 64) * U * np.stack([size, size], 1),
+                  "far dweights")
+
+
 def test_gradients_of_the_round_trip_against_differences():
     """loss = <combine(dispatch(x)), dout>: its gradient in x by combine of combine_bwd, in the
     weights by dweights, against the loss's exact dependence (it is bilinear)."""

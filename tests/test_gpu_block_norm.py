@@ -116,6 +116,25 @@ def test_norm_pitches_slices_and_places(M, K):
             assert torch.equal(p, q)
 
 
+def test_norm_rows_past_32_bit_offsets():
+    """Rows 2^30 elements apart: the fourth begins past 2^32 bytes."""
+    K, ld, M = 256, 1 << 30, 4
+    big = torch.empty((M - 1) * ld + K, dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((M, K), (ld, 1))
+    x.copy_(stream_rows(M, K, 50))
+    w = weights(K, 51).cuda()
+    res = stream_rows(M, K, 52).cuda()
+    check_norm(x.clone(), res, w, 1e-6, fq.add_rmsnorm_quant(x, w, residual=res, h=res.clone(),
+                                                            y=torch.empty_like(res)), "far")
+    dy = stream_rows(M, K, 53).cuda()
+    dx, dw = fq.add_rmsnorm_bwd(dy, x, w)
+    check_bwd(dy, x.clone(), w, None, 1e-6, dx, dw, "far")
+    want = dx.clone()
+    far = fq.add_rmsnorm_bwd(dy, x.clone(), w, dx=x)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(far, want)
+
+
 def test_norm_edge_rows():
     """Zero rows and groups, one huge value, tiny values, rows that are not finite."""
     K = 512
