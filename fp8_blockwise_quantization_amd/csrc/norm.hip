@@ -443,11 +443,14 @@ hipError_t launch_add_rmsnorm_quant(const NormArgs& a, hipStream_t stream) {
 namespace {
 
 // How the backward pass of M rows of nc chunks is cut up. A wave per row up to 256 chunks
-// (K <= 2048) once there are more than 512 rows (27.4 us at 8192 x 2048, 5.1 TB/s; 7.9 us by workgroups against
-// 8.6 us by waves at 512 rows, 12.5 against 8.9 us at 1024); wider rows by a workgroup each (49.8
-// against 55.3 us at 8192 x 4096, where a wave would hold 256 registers). Every workgroup leaves K
-// partial sums: 512 of them keep all CUs busy twice (49.8 us; 256: 60 us at 4096 x 8192 against 56,
-// 1024: 56 us at 8192 x 4096), 256 are enough up to 1024 rows (10.0 against 12.1 us at 512 x 4096).
+// (K <= 2048) once there are more than 512 rows (27.4 us at 8192 x 2048, 5.1 TB/s; 8.6 us against
+// 7.9 us by workgroups at 512 rows, 8.9 against 12.5 us at 1024); wider rows by a workgroup each
+// (49.8 against 55.3 us at 8192 x 4096, where a wave would hold 256 registers). Every workgroup
+// leaves K partial sums: 512 of them keep all CUs busy twice (56 us at 4096 x 8192, 256: 60 us; 49.8
+// us at 8192 x 4096, 1024: 56 us), 256 are enough up to 1024 rows (10.0 against 12.1 us at
+// 512 x 4096). A single one's sums are dw, without the second kernel: up to 8 rows by a wave each
+// (K = 2048: 4.5 us a call of 4 rows from the host, two kernels 6.0), up to 2 of wider rows one after
+// the other (K = 4096: 4.0 against 6.0 us, but 6.4 us for 4).
 struct BwdShape {
   int lanes;       // of a wave that share a row; 0: a workgroup takes a row
   int rw;          // lanes > 0: waves of a workgroup
@@ -455,15 +458,15 @@ struct BwdShape {
   int64_t groups;  // workgroups
 };
 BwdShape bwd_shape(int64_t M, int64_t nc) {
-  if (nc <= 64 || (nc <= 256 && M > 512)) {
+  if (nc <= 64 || (nc <= 256 && (M > 512 || M <= 8))) {
     const int lanes = nc <= 16 ? 16 : nc <= 32 ? 32 : 64;
     const int ch = nc <= 64 ? 1 : nc <= 128 ? 2 : 4;
-    const int rw = M * lanes >= 8 * 256 * 64 ? 8 : 4;
+    const int rw = M * lanes >= 8 * 256 * 64 || M <= 8 ? 8 : 4;
     const int64_t most = 256 * (8 / rw), rows = rw * 64 / lanes, g = (M + rows - 1) / rows;
     return {lanes, rw, ch, g < most ? g : most};
   }
   const int ch = M <= 512 && nc <= 1024 ? 1 : nc <= 2048 ? 2 : 4;
-  const int64_t most = M > 1024 && nc <= 1024 ? 512 : 256;
+  const int64_t most = M <= 2 ? 1 : M > 1024 && nc <= 1024 ? 512 : 256;
   return {0, 0, ch, M < most ? M : most};
 }
 
@@ -491,8 +494,12 @@ void run_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t stream) {
 
 int64_t norm_bwd_groups(int64_t M, int64_t K) { return bwd_shape(M, K / 8).groups; }
 
-hipError_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dw, hipStream_t stream) {
+hipError_t launch_add_rmsnorm_bwd(const NormBwdArgs& args, float* dw, hipStream_t stream) {
+  NormBwdArgs a = args;
   const BwdShape s = bwd_shape(a.M, a.nc);
+  // the sums of a single workgroup are dw
+  const bool direct = dw && s.groups == 1 && reinterpret_cast<uintptr_t>(dw) % 16 == 0;
+  if (direct) a.part = dw;
   if (s.groups > 0) {
     if (s.lanes && s.rw == 8) run_bwd_waves<8>(a, s, stream);
     else if (s.lanes) run_bwd_waves<4>(a, s, stream);
@@ -501,7 +508,7 @@ hipError_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, float* dw, hipStream_t s
     else run_bwd<4, false>(a, s.groups, stream);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if (!dw) return hipSuccess;
+  if (!dw || direct) return hipSuccess;
   hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)(a.nc / 4)), dim3(512), 0, stream,
                      reinterpret_cast<const f32x4*>(a.part), (int)s.groups, 2 * a.nc, dw);
   return hipGetLastError();

@@ -60,7 +60,7 @@ def check_norm(x, res, w, eps, out, what):
 
 # one row up to many, one group up to the widest row, chunks that do not fill the threads; with the
 # row counts at which lanes are dealt out differently
-SHAPES = [(8193, 1024), (8200, 1152), (8192, 2048), (600, 2176), (530, 5120), (2100, 512),
+SHAPES = [(2, 4096), (8, 2048), (6, 1024), (3, 640), (8193, 1024), (8200, 1152), (8192, 2048), (600, 2176), (530, 5120), (2100, 512),
           (8200, 128), (4100, 256), (700, 1024), (1, 128), (1, 2048), (3, 4096), (64, 4096), (5, 384), (130, 2176), (33, 5120), (7, 8192),
           (9, 11008), (4, 16384), (3, 20480), (2, 32768), (1500, 2048), (2111, 4096), (4099, 1152),
           (1100, 7168)]
@@ -254,6 +254,20 @@ def test_norm_backward_in_place_and_pitches(M, K):
         dx, dw = fq.add_rmsnorm_bwd(a, h, w, dh=b, dx=(a, b)[place])
         torch.cuda.synchronize()
         assert torch.equal(dx, ref[0]) and torch.equal(dw, ref[1])
+
+
+@pytest.mark.parametrize("M", [1, 2, 8, 600])
+def test_norm_backward_dw_of_any_alignment(M):
+    """dw that begins between 16-byte steps (a single workgroup's sums would be stored there)."""
+    K = 1024
+    dy, h, w = stream_rows(M, K, 60).cuda(), stream_rows(M, K, 61).cuda(), weights(K, 62).cuda()
+    want = fq.add_rmsnorm_bwd(dy, h, w)[1]
+    for shift in (1, 2, 3):
+        buf = torch.full((K + 8,), 5.0, device="cuda")
+        fq.add_rmsnorm_bwd(dy, h, w, dw=buf[shift:shift + K])
+        torch.cuda.synchronize()
+        assert torch.equal(buf[shift:shift + K], want)
+        assert bool((buf[:shift] == 5).all()) and bool((buf[shift + K:] == 5).all())
 
 
 def test_norm_backward_against_differences():
