@@ -154,12 +154,23 @@ __global__ __launch_bounds__(256) void rope_kv_append_kernel(RopeArgs args) {
       float wa[8], wb[8];
       widen8(has_a ? w[ca] : u32x4{0u, 0u, 0u, 0u}, wa);
       widen8(has_b ? w[cb] : u32x4{0u, 0u, 0u, 0u}, wb);
+      // widened before they are squared: float32's squares end at |x| = 2^64, bf16 does not
       double ss = 0.0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss += (double)(ua[k] * ua[k]) + (double)(ub[k] * ub[k]);
+      for (int k = 0; k < 8; ++k) {
+        const double x = (double)ua[k], y = (double)ub[k];
+        ss = __builtin_elementwise_fma(x, x, __builtin_elementwise_fma(y, y, ss));
+      }
 #pragma unroll
       for (int o = 1; o < G; o <<= 1) ss += __shfl_xor(ss, o, 64);
       r = rsqrt(ss * args.inv_dim + (double)a.eps);
+      // a head with an infinity or a NaN has no norm: NaN throughout, not r = 0 and zeros
+      if (!(ss < __builtin_inf())) r = __builtin_nan("");
+      if (ss > 0x1p100) {  // so far out x w and its rotation could leave float32
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ua[k] *= 0x1p-64f, ub[k] *= 0x1p-64f;
+        r *= 0x1p64;
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) ua[k] *= wa[k], ub[k] *= wb[k];  // exact: 8 + 8 bits
     }

@@ -216,7 +216,10 @@ typedef struct {
  * page_size >= 1, num_pages * page_size < 2^62, T * (q_heads + 2 kv_heads) < 2^25, eps as for
  * fp8rl_add_rmsnorm_quant where norms are given; bf16 pointers 16-byte and codes 8-byte aligned,
  * the table 16-byte, pitches and strides multiples of 8 elements, ld_* >= the columns, page_stride
- * (with more than one page), slot_stride and head_stride >= head_dim. A NaN stores a NaN code.
+ * (with more than one page), slot_stride and head_stride >= head_dim. A NaN stores a NaN code. The
+ * head norms take any finite bf16 x (weights below 2^60; x * weight is formed in float32, where a
+ * product below 2^-126 loses bits); a normalised head that holds an infinity or a NaN comes out as
+ * NaN in every column.
  * T == 0 returns FP8RL_OK.
  */
 fp8rl_status fp8rl_rope_kv_append(const fp8rl_rope_kv_args* args, void* stream);

@@ -294,3 +294,35 @@ def test_binding_refusals_on_device():
         fq.moe_sort(torch.zeros((2, 2), device="cuda"), 4)
     with pytest.raises(ValueError):
         fq.moe_sort(torch.zeros((2, 4), dtype=torch.int32, device="cuda")[:, ::2], 4)
+
+
+@pytest.mark.parametrize("cache8,q8", [(True, True), (False, False)])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("T", [7, 2100])
+def test_head_norms_of_far_values(T, pairs, cache8, q8):
+    """Heads whose squares leave float32 are normalised like any other (the bounds are those of the
+    module); a head with an infinity or a NaN is NaN throughout, and only that head."""
+    print(f"[append] far heads T={T} pairs={pairs} cache8={cache8}", flush=True)
+    H, D = 2, 128
+    c = Case(T, H, H, D, 96, pairs=pairs, norms=True, cache8=cache8, q8=q8, seed=21)
+    c.slots = torch.arange(T, device="cuda")
+    g = torch.Generator().manual_seed(22)
+    x = torch.randn((T, H, D), generator=g).clamp(-3.5, 3.5)
+    x[0] *= 2.0 ** 65
+    x[1] *= 2.0 ** 126                       # up to bf16's largest
+    x[2, 0] = 2e19                           # one far head beside an ordinary one
+    x[3] *= 2.0 ** 50                        # where the kernel's own scaling begins
+    x[4, 0, 5], x[4, 0, 99] = float("inf"), float("-inf")
+    x[5, 1, 127] = float("nan")
+    x[T - 1, 1] *= 2.0 ** 100
+    c.q = c.k = x.reshape(T, H * D).to(torch.bfloat16).cuda()
+    q = c.call().view(T, H, D)
+    torch.cuda.synchronize()
+    k = torch.stack([c.kc[t // c.page, t % c.page] for t in range(T)])
+    bad = torch.zeros((T, H), dtype=torch.bool)
+    bad[4, 0] = bad[5, 1] = True
+    for got, weight, scale, what in ((q, c.qw, c.qs, "q"), (k, c.kw, c.ks, "k")):
+        lost = (got & 0x7F) == 0x7F if scale is not None else torch.isnan(got)
+        assert bool(lost[bad].all()) and not bool(lost[~bad].any())
+        want, size = c.turned(c.k, weight)
+        check_values(got[~bad], want[~bad.numpy()], size[~bad.numpy()], scale, what)
