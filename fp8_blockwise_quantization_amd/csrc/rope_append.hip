@@ -32,13 +32,23 @@ struct RopeArgs {
 
 // A float64 on its way through float32 to a type of far fewer bits: cut off, and the last bit set
 // where something was (rounding to odd), so that the second rounding sees what the first dropped.
+// Less than 16 float64 units past a float32 value are taken for that value: an exact tie between
+// two codes (a token at position 0, whose rotation is the identity, can have one) arrives here at
+// most 5 units too far out, never short of it, since the reciprocal of the scale is raised (up()).
 __device__ __forceinline__ float narrow(double d) {
   const uint64_t u = __builtin_bit_cast(uint64_t, d);
-  const uint32_t lo = (uint32_t)u, rest = (lo & 0x1FFFFFFFu) + 0x1FFFFFFFu;  // bit 29: not all zero
+  const uint32_t lo = (uint32_t)u;
+  const uint32_t rest = (lo & 0x1FFFFFFFu) + 0x1FFFFFF0u;  // bit 29: 16 units or more
   const uint64_t odd = (u & 0xFFFFFFFF00000000u) | ((lo | rest) & 0xE0000000u);
   return (float)__builtin_bit_cast(double, odd);
 }
 __device__ __forceinline__ float narrow(float f) { return f; }
+
+// A correctly rounded reciprocal of S, raised by one or two units, so that it is not below 1 / S
+// and a product with it not below the quotient. Quotients that go through float32 to the nearest
+// keep their bits: x * up(1 / S) is within 2^-50.6 of x / S, whose distance from a float32
+// midpoint is more than 2^-49 (div_by_scale).
+__device__ __forceinline__ double up(double r) { return r * (1.0 + 0x1p-52); }
 
 // (x, y) -> f (x cos - y sin, y cos + x sin), in the type of f.
 template <typename F>
@@ -74,11 +84,11 @@ __device__ __forceinline__ void finish(float (&ua)[8], float (&ub)[8], const flo
 
 template <int G, int U>
 __global__ __launch_bounds__(256) void rope_kv_append_kernel(RopeArgs args) {
-  __shared__ double recip[3];  // of the scales of q, k and v
+  __shared__ double recip[3];  // of the scales of q, k and v, raised
   const fp8rl_rope_kv_args& a = args.a;
   if (threadIdx.x < 3) {
     const float* sp = threadIdx.x == 0 ? a.q_scale : threadIdx.x == 1 ? a.k_scale : a.v_scale;
-    if (sp) recip[threadIdx.x] = recip_f64(*sp);
+    if (sp) recip[threadIdx.x] = up(recip_f64(*sp));
   }
   const unsigned wave =
       (unsigned)__builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));

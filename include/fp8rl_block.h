@@ -201,8 +201,9 @@ typedef struct {
  * token,
  *   u = x * weight / sqrt(mean(x^2) + eps)     (q and k, where q_weight and k_weight are given)
  *   w[a] = u[a] cos - u[b] sin,  w[b] = u[b] cos + u[a] sin     for every rotated pair (a, b)
- * rounded once: to bf16 (formed in float32), or to the E4M3 code nearest to w / scale (formed in
- * float64; columns that are not rotated, and v, as fp8rl_quant_bf16_per_tensor rounds them)
+ * rounded once: to bf16 (formed in float32), or to the E4M3 code nearest to w / scale, ties to the
+ * even one (formed in float64: a quotient that lies within 2^-48 of its size from a tie may round
+ * as the tie; columns that are not rotated, and v, as fp8rl_quant_bf16_per_tensor rounds them)
  * (saturating). q goes to q_out, k (and v, neither normalised nor rotated) to row
  *   cache + page * page_stride + place * slot_stride + head * head_stride,
  *   page = slot / page_size, place = slot % page_size,

@@ -326,3 +326,31 @@ def test_head_norms_of_far_values(T, pairs, cache8, q8):
         assert bool(lost[bad].all()) and not bool(lost[~bad].any())
         want, size = c.turned(c.k, weight)
         check_values(got[~bad], want[~bad.numpy()], size[~bad.numpy()], scale, what)
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+def test_ties_at_position_0_go_to_the_even_code(pairs):
+    """Where the rotation is the identity, a quotient can lie exactly between two codes. A tie needs
+    a scale whose odd part fits a bf16 value's eight bits: all of them, against every value whose
+    quotient lies in the codes' range, give the plain store's codes (none of these quotients lies
+    within float32's error of a tie without being one: they differ by 1 / (31 * 255) or more)."""
+    one = lambda x: torch.tensor([x], dtype=torch.float32, device="cuda")  # noqa: E731
+    D, H = 128, 8
+    tab = torch.cat([torch.ones((1, D // 2)), torch.zeros((1, D // 2))], dim=1).cuda()
+    mant = np.arange(128, 256, dtype=np.float64)
+    values = np.concatenate([mant * 2.0 ** e for e in range(-34, 4)])
+    for odd in range(1, 256, 2):
+        s = odd * 2.0 ** -12
+        x = values[(values / s > 2.0 ** -11) & (values / s < 470)]
+        x = np.concatenate([x, -x])
+        T = -(-x.size // (H * D))
+        x = torch.from_numpy(np.resize(x, (T, H * D))).to(torch.bfloat16).cuda()
+        kc = torch.zeros((T, 1, H, D), dtype=torch.uint8, device="cuda")
+        vc = torch.zeros_like(kc)
+        q = fq.rope_kv_append(x, x, x, torch.zeros(T, dtype=torch.int64, device="cuda"), tab,
+                              torch.arange(T, device="cuda"), kc, vc, interleaved=pairs,
+                              q_scale=one(s), k_scale=one(s), v_scale=one(s))
+        want = fq.quant_per_tensor(x, one(s))
+        torch.cuda.synchronize()
+        for got in (q, kc.view(T, -1), vc.view(T, -1)):
+            assert torch.equal(got, want), s
