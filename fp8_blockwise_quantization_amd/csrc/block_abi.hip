@@ -147,8 +147,8 @@ fp8rl_status fp8rl_moe_dispatch(const uint16_t* x, int64_t ld_x, const int32_t* 
   if (fp8rl_status s = check_rows(x, ld_x, N)) return s;
   if (fp8rl_status s = check_rows(out, ld_out, N)) return s;
   if (!aligned(pos, 4)) return FP8RL_ERR_ALIGN;
-  // a wave per 2048 values of a row, below 2^32 threads in a grid
-  if (T * ((N + 2047) / 2048) >= (int64_t{1} << 26)) return FP8RL_ERR_SHAPE;
+  // a wave per 2048 values of a row, four to a workgroup: below 2^32 threads in a grid
+  if (T * ((N + 2047) / 2048) > (int64_t{1} << 26) - 4) return FP8RL_ERR_SHAPE;
   fp8rl::MoeArgs a{};
   a.x = x, a.out = out, a.pos = pos;
   a.ld_x = ld_x, a.ld_out = ld_out;

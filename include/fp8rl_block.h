@@ -127,7 +127,7 @@ size_t fp8rl_moe_sort_workspace_bytes(int64_t T, int32_t top_k, int32_t E);
  *   x   : bf16 [T][ld_x]          pos : [T][top_k] int32, its rows distinct (fp8rl_moe_sort's)
  *   out : bf16 [R][ld_out], not overlapping x
  * Requires N % 8 == 0, pitches multiples of 8 and >= N, 16-byte aligned rows, 1 <= top_k <= 64,
- * T < 2^24, T * ceil(N / 2048) < 2^26.
+ * T < 2^24, T * ceil(N / 2048) <= 2^26 - 4.
  */
 fp8rl_status fp8rl_moe_dispatch(const uint16_t* x, int64_t ld_x, const int32_t* pos, int64_t T,
                                 int32_t top_k, int64_t N, uint16_t* out, int64_t R, int64_t ld_out,

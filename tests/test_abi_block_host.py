@@ -292,3 +292,12 @@ def test_python_binding_refuses_host_tensors():
         with pytest.raises(ValueError):
             fq.rope_kv_append(q, bf(2, 128), bf(2, 128), None, None, None, bf(1, 16, 1, 128),
                               bf(1, 16, 1, 128))
+
+
+@pytest.mark.parametrize("T,pieces", [(24573, 2731), (1082401, 62), (8191, 8193)])
+def test_dispatch_refuses_a_grid_of_2_to_the_32_threads(L, T, pieces):
+    """2^26 - 3 waves or more would round up to 2^24 workgroups of 256 threads, which HIP does not
+    launch: refused by the documented bound, not by the launch."""
+    assert (1 << 26) - 3 <= T * pieces < 1 << 26
+    N = 2048 * pieces
+    assert L.fp8rl_moe_dispatch(A, N, A, T, 1, N, A, 8, N, None) == ESHAPE
