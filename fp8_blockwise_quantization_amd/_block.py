@@ -13,11 +13,13 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import os
 
 import torch
 
 from . import _lib
 from ._lib import FP8RL_SCALE_FP32, _check, _on_stream, _scale_code
+from .build import MARSHAL_PATH
 
 FP8RL_IDS_I32 = 0
 FP8RL_IDS_I64 = 1
@@ -102,7 +104,9 @@ def _marshal():
         try:
             from . import _marshal as module
         except ImportError as e:
-            raise RuntimeError("the argument marshalling is not built: run "
+            what = (f"cannot be loaded ({e}); build it again with the torch that is installed"
+                    if os.path.exists(MARSHAL_PATH) else "is not built")
+            raise RuntimeError(f"the argument marshalling {what}: run "
                                "`python -m fp8_blockwise_quantization_amd.build`") from e
         _m = module
     return _m

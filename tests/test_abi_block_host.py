@@ -7,6 +7,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -301,3 +302,16 @@ def test_dispatch_refuses_a_grid_of_2_to_the_32_threads(L, T, pieces):
     assert (1 << 26) - 3 <= T * pieces < 1 << 26
     N = 2048 * pieces
     assert L.fp8rl_moe_dispatch(A, N, A, T, 1, N, A, 8, N, None) == ESHAPE
+
+
+def test_a_marshalling_module_that_does_not_load_says_why(monkeypatch, tmp_path):
+    """Built but not loadable (another torch's, say) is told apart from not built."""
+    monkeypatch.setattr(_block, "_m", None)
+    monkeypatch.delattr(fq, "_marshal", raising=False)
+    monkeypatch.setitem(sys.modules, fq.__name__ + "._marshal", None)  # its import fails
+    with pytest.raises(RuntimeError, match="cannot be loaded .*_marshal.*build it again") as e:
+        _block._marshal()
+    assert isinstance(e.value.__cause__, ImportError)
+    monkeypatch.setattr(_block, "MARSHAL_PATH", str(tmp_path / "none.so"))
+    with pytest.raises(RuntimeError, match="is not built"):
+        _block._marshal()
