@@ -1,7 +1,9 @@
 """Build the gfx950 HIP library ``libfp8rl.so`` in-tree with hipcc, and beside it the compiled argument
 marshalling of the operators between the linears (``_marshal``, host code only) with the C++ compiler.
 
-Usage: ``python -m fp8_blockwise_quantization_amd.build`` (or call ``build()``).
+Usage: ``python -m fp8_blockwise_quantization_amd.build`` (or call ``build()``). With
+``--library-only`` (``build(marshal=False)``) the library alone, for who calls the C ABI or the
+linears' binding: the Python and torch headers, which the marshalling needs, may then be absent.
 """
 
 from __future__ import annotations
@@ -42,6 +44,17 @@ def hipcc_path() -> str:
     raise RuntimeError("hipcc not found: the HIP toolchain (ROCm) is required to build libfp8rl")
 
 
+def cxx_path() -> str:
+    """A host C++ compiler: the system's, else the one that comes with hipcc."""
+    for name in ("g++", "c++", "clang++", "amdclang++"):
+        if path := shutil.which(name):
+            return path
+    path = os.path.join(os.path.dirname(hipcc_path()), "amdclang++")
+    if os.path.exists(path):
+        return path
+    raise RuntimeError("a C++ compiler is required to build the argument marshalling")
+
+
 def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -56,12 +69,9 @@ def build_marshal(verbose: bool = False) -> str:
     returns the extension module's path."""
     import torch
 
-    cxx = shutil.which("g++") or shutil.which("c++") or shutil.which("clang++")
-    if cxx is None:
-        raise RuntimeError("a C++ compiler is required to build the argument marshalling")
     troot = os.path.dirname(torch.__file__)
     tmp = MARSHAL_PATH + ".tmp"
-    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+    cmd = [cxx_path(), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(troot, "include"),
            "-isystem", sysconfig.get_paths()["include"], MARSHAL_SOURCE, "-o", tmp,
@@ -72,10 +82,11 @@ def build_marshal(verbose: bool = False) -> str:
     return MARSHAL_PATH
 
 
-def build(verbose: bool = False, extra_flags=(), out_path: str | None = None) -> str:
+def build(verbose: bool = False, extra_flags=(), out_path: str | None = None,
+          marshal: bool = True) -> str:
     """Compile every HIP source into ``libfp8rl.so`` next to this file, and the marshalling module
-    that links to it (or, with ``out_path``, the library alone into that file); returns the
-    library's path."""
+    that links to it (unless ``marshal`` is false; with ``out_path``, the library alone into that
+    file); returns the library's path."""
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     out = out_path or LIB_PATH
     tmp = out + ".tmp"
@@ -83,10 +94,12 @@ def build(verbose: bool = False, extra_flags=(), out_path: str | None = None) ->
            "-o", tmp, *srcs]
     _run(cmd, verbose)
     os.replace(tmp, out)
-    if out_path is None:
+    if out_path is None and marshal:
         build_marshal(verbose)
     return out
 
 
 if __name__ == "__main__":
-    print(build(verbose=True))
+    if set(sys.argv[1:]) - {"--library-only"}:
+        sys.exit("usage: python -m fp8_blockwise_quantization_amd.build [--library-only]")
+    print(build(verbose=True, marshal="--library-only" not in sys.argv))
