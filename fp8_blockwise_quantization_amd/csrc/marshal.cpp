@@ -8,6 +8,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <ATen/ops/empty.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
@@ -381,8 +382,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return PyLong_FromLong(F(args));
   } catch (const Raised&) {
     return nullptr;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own, as its functions raise them (a workspace that does not fit, say)
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }

@@ -295,3 +295,31 @@ def test_norm_backward_against_differences():
         e[k] = s
         num = (loss(H, W + e) - loss(H, W - e)) / (2 * s)
         assert abs(num - float(dw[k])) <= 1e-4 * (1 + abs(num))
+
+
+def test_a_workspace_that_does_not_fit_raises_torchs_error():
+    """As torch.empty would: the type that a caller who frees memory and tries again looks for."""
+    M, K = 1025, 32768
+    dy, h, w = stream_rows(M, K, 70).cuda(), stream_rows(M, K, 71).cuda(), weights(K, 72).cuda()
+    dx, dw = torch.empty_like(dy), torch.empty(K, device="cuda")
+    need = fq.fp8rl_add_rmsnorm_bwd_workspace_bytes(M, K)
+    assert need == 32 << 20
+    want = [t.clone() for t in fq.add_rmsnorm_bwd(dy, h, w, dx=dx, dw=dw)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction(torch.cuda.memory_reserved() / total)
+    held = []
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            while len(held) < 10000:  # what torch still holds of free memory
+                held.append(torch.empty(need, dtype=torch.uint8, device="cuda"))
+        with pytest.raises(torch.OutOfMemoryError):
+            fq.add_rmsnorm_bwd(dy, h, w, dx=dx, dw=dw)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    del held
+    dx.zero_()
+    got = fq.add_rmsnorm_bwd(dy, h, w, dx=dx, dw=dw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
