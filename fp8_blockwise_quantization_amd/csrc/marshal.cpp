@@ -205,8 +205,10 @@ int moe_sort(PyObject* const* a) {
                                c10::toString(ids.scalar_type()));
   if (!ids.is_contiguous()) raise(PyExc_ValueError, "topk_ids must be contiguous");
   const int64_t T = ids.size(0), k = ids.size(1), E = integer(a[1]);
+  if (E < 0 || E >= int64_t{1} << 31)
+    raise(PyExc_ValueError, "E is " + std::to_string(E) + ", out of range");
   // (what does not fit the C types is out of its range as well)
-  const int32_t k32 = k > 65 ? 65 : (int32_t)k, e32 = E < 0 || E > 1025 ? 1025 : (int32_t)E;
+  const int32_t k32 = k > 65 ? 65 : (int32_t)k, e32 = E > 1025 ? 1025 : (int32_t)E;
   auto* off = flat<int32_t>(a[2], "expert_offsets", dev, at::kInt, E + 1);
   auto* rows = flat<int32_t>(a[3], "row_ids", dev, at::kInt, T * k);
   auto* pos = dense<int32_t>(a[4], "pos", dev, at::kInt, T, k);

@@ -304,3 +304,16 @@ def test_gradients_of_the_round_trip_against_differences():
         e[t, j] = 1.0
         num = loss(X, W + e) - loss(X, W)
         assert abs(num - float(dw[t, j])) <= 1e-5 * np.abs(X[t] * D[t]).sum()
+
+
+def test_sort_refuses_numbers_of_experts_out_of_range():
+    """Past the C type, and at the ends of 64 bits, where E + 1 has no value."""
+    ids = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    for E in (2 ** 63 - 1, -2 ** 63, 2 ** 31, -1):
+        with pytest.raises(ValueError, match=f"E is {E}, out of range"):
+            fq.moe_sort(ids, E, expert_offsets=torch.zeros(5, dtype=torch.int32, device="cuda"))
+    for E in (0, 1025):
+        with pytest.raises(fq.Fp8rlError):
+            fq.moe_sort(ids, E)
+    with pytest.raises(OverflowError):
+        fq.moe_sort(ids, 2 ** 63, expert_offsets=torch.zeros(5, dtype=torch.int32, device="cuda"))
