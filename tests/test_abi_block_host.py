@@ -315,3 +315,13 @@ def test_a_marshalling_module_that_does_not_load_says_why(monkeypatch, tmp_path)
     monkeypatch.setattr(_block, "MARSHAL_PATH", str(tmp_path / "none.so"))
     with pytest.raises(RuntimeError, match="is not built"):
         _block._marshal()
+
+
+def test_sort_workspace_begins_past_one_workgroup(L):
+    """4096 choices are one workgroup's, however they are shaped; 256 workgroups at most."""
+    need = L.fp8rl_moe_sort_workspace_bytes
+    for T, k in ((4096, 1), (512, 8), (64, 64), (585, 7), (0, 8)):
+        assert need(T, k, 128) == 0, (T, k)
+    for T, k, blocks in ((4097, 1, 2), (513, 8, 2), (65, 64, 2), (586, 7, 2), (1 << 20, 1, 256),
+                         ((1 << 24) - 1, 64, 256)):
+        assert need(T, k, 128) == blocks * 128 * 4, (T, k)

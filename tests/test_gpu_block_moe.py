@@ -317,3 +317,34 @@ def test_sort_refuses_numbers_of_experts_out_of_range():
             fq.moe_sort(ids, E)
     with pytest.raises(OverflowError):
         fq.moe_sort(ids, 2 ** 63, expert_offsets=torch.zeros(5, dtype=torch.int32, device="cuda"))
+
+
+# one workgroup sorts up to 4096 choices, a tile of 256 in each of its 16 waves; more take two kernels
+@pytest.mark.parametrize("T,k,E", [(513, 1, 128), (1025, 1, 128), (4095, 1, 128), (4096, 1, 128),
+                                   (4097, 1, 128), (512, 8, 128), (513, 8, 128), (585, 7, 1024),
+                                   (586, 7, 1024), (64, 64, 1), (65, 63, 1000), (257, 16, 17)])
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_sort_around_a_full_workgroup(T, k, E, dtype):
+    print(f"[sort] T={T} k={k} E={E} {dtype}", flush=True)
+    blocks = -(-T * k // 4096)
+    assert fq.fp8rl_moe_sort_workspace_bytes(T, k, E) == (4 * blocks * E if blocks > 1 else 0)
+    check_sort(choices(T, k, E, T + k), E, dtype)
+    check_sort(choices(T, k, E, T + k + 1, "one"), E, dtype)
+
+
+def test_sort_at_the_most_blocks():
+    """256 blocks of 4096 choices, and the first call past them, whose blocks take more."""
+    E = 64
+    for n in (256 * 4096, 256 * 4096 + 1):
+        assert fq.fp8rl_moe_sort_workspace_bytes(n, 1, E) == 4 * 256 * E
+        g = torch.Generator(device="cuda").manual_seed(n)
+        ids = torch.randint(-1, E, (n, 1), generator=g, device="cuda")
+        off, rows, pos = fq.moe_sort(ids, E)
+        key = torch.where(ids >= 0, ids, E).view(-1)
+        order = torch.sort(key, stable=True).indices
+        m = int((key < E).sum())
+        assert int(off[E]) == m
+        assert torch.equal(rows[:m].long(), order[:m]) and bool((rows[m:] == -1).all())
+        assert torch.equal(pos.view(-1)[order[:m]].long(), torch.arange(m, device="cuda"))
+        assert bool((pos.view(-1)[order[m:]] == -1).all())
+        assert torch.equal(torch.diff(off).long(), torch.bincount(key, minlength=E + 1)[:E])
