@@ -16,6 +16,8 @@
 // with E4M3 outputs, 155 MB, one: 43 us, three: 36 us but 39 against 37 us with bf16 outputs), one
 // where that leaves CUs idle. With bf16 outputs memory bounds it (206 MB in 37.4 us, 5.5 TB/s),
 // with E4M3 ones the conversions take about as long as the bytes (16384 tokens: 63 us, 4.9 TB/s).
+// Head norms, formed in float64, add to that: with a bf16 q and an E4M3 cache 38.2 against 33.0 us,
+// all in E4M3 42.0 against 34.1 us, all in bf16 39.3 against 37.5 us.
 #include "block_ops.hpp"
 
 namespace fp8rl {
