@@ -56,7 +56,8 @@ extern "C" {
  * Requires K % 128 == 0, K <= 32768, M < 2^22; bf16 pointers 16-byte aligned and their
  * pitches multiples of 8, xq 16-byte aligned and ld_xq a multiple of 16. A row whose sum of squares
  * is not finite in float32 (an infinity, a NaN, magnitudes past about 2^63) comes out with NaN
- * scales and NaN y. Deterministic.
+ * scales and NaN y. h * weight is formed in float32: weights below 2^60 (a product below 2^-126
+ * loses bits). Deterministic.
  */
 fp8rl_status fp8rl_add_rmsnorm_quant(const uint16_t* x, int64_t ld_x, const uint16_t* residual,
                                      int64_t ld_res, const uint16_t* weight, float eps, int64_t M,
