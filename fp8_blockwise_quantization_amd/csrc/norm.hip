@@ -420,11 +420,10 @@ void run_norm(const NormArgs& a, hipStream_t stream) {
 // 54.3 us (K = 1152), but 6.4 against 5.2 us at 2048 rows of K = 1024, where a quarter of the waves
 // is too few to hide the loads. Wider rows by about four waves, 2 to 4 chunks a lane; up to 512
 // rows (two a CU) by one chunk a lane, up to 16 waves: 4.0 against 4.8 us (64 rows, K = 4096), 4.7
-// against 6.1 us (K = 8192). Four waves at one or two chunks a lane (K of
-// 1664 to 2048 and 3200 to 4096) have a form with their number known (its sums unrolled): 42.2
-// against 43.8 us at 8192 x 4096. The widths that run four waves at three or four chunks (4736 to
-// 6144, 6272 to 8192) would gain less from one and have none: 51.6 against 49.9 us at 8192 x 5120,
-// 43.2 against 42.5 us at 4096 x 8192, even at 4096 x 7168 with power-of-two scales.
+// against 6.1 us (K = 8192). Four waves at one or two chunks a lane (K of 1664 to 2048 and 3200 to
+// 4096) have a form with their number known (its sums unrolled): 42.2 against 43.8 us at 8192 x
+// 4096. Four waves at three or four chunks (4736 to 6144, 6272 to 8192) have none, which would save
+// 1 to 3 %: 49.9 against 51.6 us at 8192 x 5120, 42.5 against 43.2 us at 4096 x 8192.
 // 8192 x 4096 is 134 MB read and 102 MB written, 5.6 TB/s: more than a copy (5.2 - 5.5 TB/s), less
 // than reads or writes alone (6.4 and 6.9 TB/s). With power-of-two scales, whose codes wait for the
 // row's sum, 42.9 against 40.6 us.

@@ -324,7 +324,8 @@ def test_head_norms_of_far_values(T, pairs, cache8, q8):
     for got, weight, scale, what in ((q, c.qw, c.qs, "q"), (k, c.kw, c.ks, "k")):
         lost = (got & 0x7F) == 0x7F if scale is not None else torch.isnan(got)
         assert bool(lost[bad].all()) and not bool(lost[~bad].any())
-        want, size = c.turned(c.k, weight)
+        with np.errstate(invalid="ignore"):  # the bad heads, which are not compared
+            want, size = c.turned(c.k, weight)
         check_values(got[~bad], want[~bad.numpy()], size[~bad.numpy()], scale, what)
 
 
