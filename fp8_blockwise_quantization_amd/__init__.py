@@ -70,6 +70,12 @@ from ._block import (  # noqa: F401
     fp8rl_moe_sort_workspace_bytes,
     fp8rl_rope_kv_append,
 )
+from ._attn import (  # noqa: F401
+    EXPORTED_ATTN,
+    fp8rl_attn_decode,
+    fp8rl_attn_decode_workspace_bytes,
+    fp8rl_kv_read,
+)
 
 # Short aliases.
 quant_weight = fp8rl_quant_weight_blk128
@@ -96,3 +102,5 @@ moe_dispatch = fp8rl_moe_dispatch
 moe_combine = fp8rl_moe_combine
 moe_combine_bwd = fp8rl_moe_combine_bwd
 rope_kv_append = fp8rl_rope_kv_append
+attn_decode = fp8rl_attn_decode
+kv_read = fp8rl_kv_read

@@ -1,0 +1,91 @@
+// Host-side launchers and shared device helpers of attention (arguments are validated in
+// attn_abi.hip before these are called).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "block_ops.hpp"
+#include "fp8rl_attn.h"
+
+namespace fp8rl {
+
+// ---- attn_decode.hip
+size_t attn_decode_workspace(int64_t B, int q_heads, int kv_heads, int head_dim, int64_t max_keys,
+                             int window);
+hipError_t launch_attn_decode(const fp8rl_attn_decode_args& a, void* workspace, hipStream_t stream);
+
+// ---- kv_read.hip
+hipError_t launch_kv_read(const fp8rl_kv_read_args& a, hipStream_t stream);
+
+// ---------------------------------------------------------------------------------------------
+// Device helpers
+// ---------------------------------------------------------------------------------------------
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// tanh of a capped score: 1 - 2 / (e^2x + 1), off by a few 2^-24 (not relative to small x, which is
+// what a score in units of cap needs); exact at both ends, where e^2x is 0 or infinite.
+__device__ __forceinline__ float tanh_cap(float x) {
+  return 1.f - 2.f * __builtin_amdgcn_rcpf(exp2_fast(2.f * kLog2e * x) + 1.f);
+}
+
+// Max (sum) over the lanes that differ in bit 4 or 5 of their number, in each of them.
+__device__ __forceinline__ float max_rows(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_rows(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Four E4M3 codes as two words of bf16 or of fp16 pairs (exact).
+__device__ __forceinline__ u32x2 codes_bf16(uint32_t w) {
+  return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true))};
+}
+__device__ __forceinline__ u32x2 codes_f16(uint32_t w) {
+  return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true))};
+}
+
+// The page that holds a key: key / page_size by a product with ceil(2^62 / page_size), exact for
+// keys and page sizes below 2^31 (the product's error, key * (page_size - 1) at most, is below 2^62).
+struct PageOf {
+  uint64_t reciprocal;
+  int page_size;
+  __host__ explicit PageOf(int size)
+      : reciprocal(((uint64_t{1} << 62) + (uint64_t)size - 1) / (uint64_t)size), page_size(size) {}
+  PageOf() = default;
+  __device__ __forceinline__ int operator()(int key) const {
+    return (int)__umul64hi((uint64_t)(uint32_t)key << 2, reciprocal);
+  }
+};
+
+// The number of a row's document: how many of offsets[1 .. n] (not decreasing) are <= row, which is
+// the same in all lanes; n at most. 64 samples a step.
+__device__ __forceinline__ int document_of(const int32_t* offsets, int n, int row, int lane) {
+  int lo = 0, hi = n;  // offsets[lo] <= row (by convention for 0) and the answer is in [lo, hi]
+  while (hi > lo) {
+    const int step = (hi - lo + 63) >> 6;
+    const int at = lo + (lane + 1) * step;
+    const bool below = at <= hi && offsets[at] <= row;
+    lo += __popcll(__ballot(below)) * step;  // the last sample that is not past the row
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+}  // namespace fp8rl

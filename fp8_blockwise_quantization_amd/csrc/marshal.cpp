@@ -1,4 +1,4 @@
-// Argument marshalling of the operators between the linears, from Python: each function checks the
+// Argument marshalling of the operators between the linears and of attention, from Python: each function checks the
 // tensors of one call (device, type, shape, layout), passes their addresses and pitches to the C
 // entry point and returns its status. No arithmetic, no copies.
 //
@@ -13,6 +13,7 @@
 
 #include <string>
 
+#include "fp8rl_attn.h"
 #include "fp8rl_block.h"
 
 namespace {
@@ -373,6 +374,113 @@ int rope_kv_append(PyObject* const* a) {
   return status;
 }
 
+constexpr int64_t kInt32 = (int64_t{1} << 31) - 1;
+
+int32_t int32_of(PyObject* o, const char* name) {
+  const int64_t v = integer(o);
+  if (v < -kInt32 - 1 || v > kInt32)
+    raise(PyExc_ValueError, std::string(name) + " is " + std::to_string(v) + ", out of range");
+  return (int32_t)v;
+}
+
+// A pair of paged caches, their scales and the page table into the fields that their readers share.
+template <typename Args>
+void paged(Args& r, PyObject* k_cache, PyObject* v_cache, PyObject* k_scale, PyObject* v_scale,
+           PyObject* page_table, int64_t B, int dev) {
+  const at::Tensor &kc = tensor(k_cache, "k_cache", dev), &vc = tensor(v_cache, "v_cache", dev);
+  if (kc.dim() != 4)
+    raise(PyExc_ValueError, "k_cache must be 4-D: [page][place][head][column]");
+  const int64_t pages = kc.size(0), page = kc.size(1), heads = kc.size(2), D = kc.size(3);
+  if (page > kInt32 || heads > kInt32 || D > kInt32)
+    raise(PyExc_ValueError, "k_cache has a dimension past 2^31");
+  const at::ScalarType kind = none(k_scale) ? kBf16 : at::kByte;
+  need_type(kc, "k_cache", kind);
+  need_type(vc, "v_cache", kind);
+  need_shape(vc, "v_cache", kc.sizes());
+  if (kc.numel() > 0) {
+    if (kc.strides() != vc.strides())
+      raise(PyExc_ValueError, "k_cache and v_cache must have the same strides");
+    if (D > 1 && kc.stride(3) != 1)
+      raise(PyExc_ValueError, "k_cache must have unit stride along its last dimension");
+  }
+  r.k_cache = kc.data_ptr(), r.v_cache = vc.data_ptr();
+  r.k_scale = flat<float>(k_scale, "k_scale", dev, at::kFloat, 1);
+  r.v_scale = flat<float>(v_scale, "v_scale", dev, at::kFloat, 1);
+  r.num_pages = pages, r.page_size = (int32_t)page;
+  r.kv_heads = (int32_t)heads, r.head_dim = (int32_t)D;
+  // a dimension of one entry has no stride to speak of
+  r.page_stride = pages > 1 ? kc.stride(0) : 0;
+  r.slot_stride = page > 1 ? kc.stride(1) : D;
+  r.head_stride = heads > 1 ? kc.stride(2) : D;
+  const at::Tensor& table = tensor(page_table, "page_table", dev);
+  need_2d(table, "page_table");
+  if (table.size(1) > kInt32) raise(PyExc_ValueError, "page_table is too wide");
+  const Rows rt = matrix(table, "page_table", at::kInt, B, table.size(1));
+  r.page_table = (int32_t*)rt.p, r.ld_table = rt.ld, r.table_width = (int32_t)table.size(1);
+}
+
+// The heads of width D in a row of `cols` columns.
+int32_t heads_in(int64_t cols, int64_t D, const char* name) {
+  if (D <= 0 || cols % D || cols / D > kInt32)
+    raise(PyExc_ValueError, std::string(name) + " has " + std::to_string(cols) +
+                                " columns, no multiple of the head width " + std::to_string(D));
+  return (int32_t)(cols / D);
+}
+
+// q, k_cache, v_cache, page_table, lengths, sm_scale, window, cap, slopes, q_scale, k_scale, v_scale,
+// out, workspace, dev, stream
+int attn_decode(PyObject* const* a) {
+  const int dev = (int)integer(a[14]);
+  const at::Tensor &q = tensor(a[0], "q", dev), &out = tensor(a[12], "out", dev);
+  need_2d(q, "q");
+  const int64_t B = q.size(0), cols = q.size(1);
+  fp8rl_attn_decode_args r{};
+  paged(r, a[1], a[2], a[10], a[11], a[3], B, dev);
+  r.B = B, r.q_heads = heads_in(cols, r.head_dim, "q");
+  const Rows rq = matrix(q, "q", none(a[9]) ? kBf16 : at::kByte, B, cols);
+  const Rows ro = matrix(out, "out", kBf16, B, cols);
+  r.q = rq.p, r.ld_q = rq.ld, r.out = (uint16_t*)ro.p, r.ld_out = ro.ld;
+  r.q_scale = flat<float>(a[9], "q_scale", dev, at::kFloat, 1);
+  r.lengths = flat<int32_t>(a[4], "lengths", dev, at::kInt, B);
+  r.sm_scale = number(a[5]), r.window = int32_of(a[6], "window"), r.cap = number(a[7]);
+  r.slopes = flat<float>(a[8], "slopes", dev, at::kFloat, r.q_heads);
+  const Workspace ws(a[13],
+                     fp8rl_attn_decode_workspace_bytes(B, r.q_heads, r.kv_heads, r.head_dim,
+                                                       (int64_t)r.table_width * r.page_size,
+                                                       r.window),
+                     q, dev);
+  void* stream = stream_of(a[15]);
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = fp8rl_attn_decode(&r, ws.p, ws.bytes, stream);
+  Py_END_ALLOW_THREADS
+  return status;
+}
+
+// k_cache, v_cache, page_table, offsets, starts, k_scale, v_scale, k_out, v_out, dev, stream
+int kv_read(PyObject* const* a) {
+  const int dev = (int)integer(a[9]);
+  const at::Tensor &table = tensor(a[2], "page_table", dev), &k = tensor(a[7], "k_out", dev),
+                   &v = tensor(a[8], "v_out", dev);
+  need_2d(table, "page_table");
+  need_2d(k, "k_out");
+  fp8rl_kv_read_args r{};
+  const int64_t B = table.size(0), R = k.size(0);
+  paged(r, a[0], a[1], a[5], a[6], a[2], B, dev);
+  const int64_t cols = (int64_t)r.kv_heads * r.head_dim;
+  const Rows rk = matrix(k, "k_out", kBf16, R, cols), rv = matrix(v, "v_out", kBf16, R, cols);
+  r.B = B, r.R = R;
+  r.k_out = (uint16_t*)rk.p, r.ld_k = rk.ld, r.v_out = (uint16_t*)rv.p, r.ld_v = rv.ld;
+  r.offsets = flat<int32_t>(a[3], "offsets", dev, at::kInt, B + 1);
+  r.starts = flat<int32_t>(a[4], "starts", dev, at::kInt, B);
+  void* stream = stream_of(a[10]);
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = fp8rl_kv_read(&r, stream);
+  Py_END_ALLOW_THREADS
+  return status;
+}
+
 // A function of N arguments as a Python callable: its status, or NULL with the exception set.
 template <int (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -400,6 +508,8 @@ PyMethodDef kMethods[] = {FP8RL_CALL(add_rmsnorm_quant, 11),
                           FP8RL_CALL(moe_combine, 6),
                           FP8RL_CALL(moe_combine_bwd, 8),
                           FP8RL_CALL(rope_kv_append, 18),
+                          FP8RL_CALL(attn_decode, 16),
+                          FP8RL_CALL(kv_read, 11),
                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods,
