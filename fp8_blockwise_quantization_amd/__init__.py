@@ -72,8 +72,11 @@ from ._block import (  # noqa: F401
 )
 from ._attn import (  # noqa: F401
     EXPORTED_ATTN,
+    fp8rl_attn_bwd,
+    fp8rl_attn_bwd_workspace_bytes,
     fp8rl_attn_decode,
     fp8rl_attn_decode_workspace_bytes,
+    fp8rl_attn_fwd,
     fp8rl_kv_read,
 )
 
@@ -104,3 +107,5 @@ moe_combine_bwd = fp8rl_moe_combine_bwd
 rope_kv_append = fp8rl_rope_kv_append
 attn_decode = fp8rl_attn_decode
 kv_read = fp8rl_kv_read
+attn_fwd = fp8rl_attn_fwd
+attn_bwd = fp8rl_attn_bwd

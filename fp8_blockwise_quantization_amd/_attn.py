@@ -13,13 +13,16 @@ import math
 import torch
 
 from . import _lib
-from ._block import _at, _here, _marshal, _raw_stream
+from ._block import _at, _here, _marshal, _raw_stream, _shape2
 from ._lib import _check
 
 EXPORTED_ATTN = (
     "fp8rl_attn_decode",
     "fp8rl_attn_decode_workspace_bytes",
     "fp8rl_kv_read",
+    "fp8rl_attn_fwd",
+    "fp8rl_attn_bwd",
+    "fp8rl_attn_bwd_workspace_bytes",
 )
 
 
@@ -55,6 +58,16 @@ class KvReadArgs(_Args):
         ("offsets starts", _P), ("R", _I64), ("k_out v_out", _P), ("ld_k ld_v", _I64))
 
 
+class AttnArgs(_Args):
+    """fp8rl_attn_args."""
+
+    _fields_ = _Args.fields(
+        ("q k v", _P), ("ld_q ld_k ld_v Tq Tk", _I64), ("q_heads kv_heads head_dim", _I32),
+        ("docs", _I64), ("q_offsets k_offsets", _P), ("causal window", _I32), ("prefix", _P),
+        ("sm_scale cap", _F32), ("slopes out", _P), ("ld_out", _I64), ("lse dout", _P),
+        ("ld_dout", _I64), ("dq dk dv", _P), ("ld_dq ld_dk ld_dv", _I64))
+
+
 def declare_attn(L: ctypes.CDLL) -> ctypes.CDLL:
     """Set the argument and result types of these functions on a loaded copy of the library."""
     sz, ci, ptr = ctypes.c_size_t, ctypes.c_int, ctypes.POINTER
@@ -62,6 +75,9 @@ def declare_attn(L: ctypes.CDLL) -> ctypes.CDLL:
         "fp8rl_attn_decode": (ci, [ptr(AttnDecodeArgs), _P, sz, _P]),
         "fp8rl_attn_decode_workspace_bytes": (sz, [_I64, _I32, _I32, _I32, _I64, _I32]),
         "fp8rl_kv_read": (ci, [ptr(KvReadArgs), _P]),
+        "fp8rl_attn_fwd": (ci, [ptr(AttnArgs), _P]),
+        "fp8rl_attn_bwd": (ci, [ptr(AttnArgs), _P, sz, _P]),
+        "fp8rl_attn_bwd_workspace_bytes": (sz, [_I64, _I32]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -141,3 +157,63 @@ def fp8rl_kv_read(k_cache, v_cache, page_table, offsets, starts=None, k_scale=No
     _check(_marshal().kv_read(k_cache, v_cache, page_table, offsets, starts, k_scale, v_scale, k_out,
                               v_out, dev, _raw_stream(dev)), "fp8rl_kv_read")
     return k_out, v_out
+
+
+def fp8rl_attn_fwd(q, k, v, head_dim: int, q_offsets, k_offsets=None, causal: bool = True,
+                   sm_scale=None, window: int = 0, prefix=None, cap: float = 0.0, slopes=None,
+                   out=None, lse=None, stream=None):
+    """Attention of packed documents: (out, lse), bf16 [Tq][Hq * D] and float32 [Hq][Tq].
+
+    q [Tq][Hq * D], k and v [Tk][Hkv * D] are bf16 rows, e.g. column slices of one fused output;
+    document d's queries are rows q_offsets[d] .. q_offsets[d + 1] - 1 (int32, on the device), its keys
+    those of ``k_offsets`` (None: the same rows). With Lq queries and Lk keys query i is at position
+    p = i + Lk - Lq, and sees key j if (not causal or j <= p) and (no window or p - j < window), or
+    if j < prefix[d] (int32 [docs]). ``sm_scale`` is 1 / sqrt(D) unless given; ``cap`` bounds the
+    scores by cap * tanh(s / cap), ``slopes`` float32 [Hq] takes slope * |p - j| off them. Rows of no
+    document are not written. lse is the log of a query's sum of exponentials, -inf (and zeros in
+    out) where it sees no key."""
+    dev = _here(q, stream)
+    if dev < 0:
+        with _at(q, "q", stream):
+            return fp8rl_attn_fwd(q, k, v, head_dim, q_offsets, k_offsets, causal, sm_scale, window,
+                                  prefix, cap, slopes, out, lse)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        Tq, cols = _shape2(q, "q")
+        lse = torch.empty((cols // max(head_dim, 1), Tq), dtype=torch.float32, device=q.device)
+    if sm_scale is None:
+        sm_scale = 1 / math.sqrt(max(head_dim, 1))
+    _check(_marshal().attn_fwd(q, k, v, head_dim, q_offsets, k_offsets, causal, sm_scale, window,
+                               prefix, cap, slopes, out, lse, dev, _raw_stream(dev)),
+           "fp8rl_attn_fwd")
+    return out, lse
+
+
+def fp8rl_attn_bwd_workspace_bytes(Tq: int, q_heads: int) -> int:
+    return int(_attn_lib().fp8rl_attn_bwd_workspace_bytes(Tq, q_heads))
+
+
+def fp8rl_attn_bwd(dout, q, k, v, out, lse, head_dim: int, q_offsets, k_offsets=None,
+                   causal: bool = True, sm_scale=None, window: int = 0, prefix=None, cap: float = 0.0,
+                   slopes=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of fp8rl_attn_fwd: (dq, dk, dv), bf16, shaped as q, k and v, from the gradient dout
+    at its output and what it returned; the other arguments are that call's. The gradients may be
+    column slices of one fused row. Rows of no document are not written."""
+    dev = _here(dout, stream)
+    if dev < 0:
+        with _at(dout, "dout", stream):
+            return fp8rl_attn_bwd(dout, q, k, v, out, lse, head_dim, q_offsets, k_offsets, causal,
+                                  sm_scale, window, prefix, cap, slopes, dq, dk, dv, workspace)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dout.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dout.device)
+    if dv is None:
+        dv = torch.empty(v.shape, dtype=torch.bfloat16, device=dout.device)
+    if sm_scale is None:
+        sm_scale = 1 / math.sqrt(max(head_dim, 1))
+    _check(_marshal().attn_bwd(q, k, v, head_dim, q_offsets, k_offsets, causal, sm_scale, window,
+                               prefix, cap, slopes, out, lse, dout, dq, dk, dv, workspace, dev,
+                               _raw_stream(dev)), "fp8rl_attn_bwd")
+    return dq, dk, dv

@@ -21,7 +21,7 @@ LIB_NAME = "libfp8rl.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ("quant.hip", "tensor_quant.hip", "transpose_quant.hip", "gemm.hip", "fp8rl_abi.hip",
            "norm.hip", "moe.hip", "rope_append.hip", "block_abi.hip", "attn_decode.hip", "kv_read.hip",
-           "attn_abi.hip")
+           "attn_fwd.hip", "attn_bwd.hip", "attn_abi.hip")
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = "gfx950"

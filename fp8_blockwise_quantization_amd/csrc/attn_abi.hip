@@ -154,4 +154,86 @@ fp8rl_status fp8rl_kv_read(const fp8rl_kv_read_args* args, void* stream) {
   return hip_status(fp8rl::launch_kv_read(a, as_stream(stream)));
 }
 
+namespace {
+
+constexpr int64_t kMaxPitch = int64_t{1} << 24;  // 64 rows are less than 2^32 bytes apart
+
+fp8rl_status check_attn_shape(const fp8rl_attn_args& a) {
+  if (a.Tq < 0 || a.Tk < 0 || a.Tq >= (int64_t{1} << 24) || a.Tk >= (int64_t{1} << 24))
+    return FP8RL_ERR_SHAPE;
+  if (a.docs < 0 || a.docs >= (int64_t{1} << 20)) return FP8RL_ERR_SHAPE;
+  if (fp8rl_status s = check_heads(a.q_heads, a.kv_heads, a.head_dim, 128)) return s;
+  if (((a.Tq > a.Tk ? a.Tq : a.Tk) / 128 + a.docs) * a.q_heads >= (int64_t{1} << 24))
+    return FP8RL_ERR_SHAPE;
+  if (a.causal != 0 && a.causal != 1) return FP8RL_ERR_ARG;
+  if (fp8rl_status s = check_scores(a.sm_scale, a.window, a.cap)) return s;
+  return a.sm_scale > 0.f ? FP8RL_OK : FP8RL_ERR_ARG;
+}
+
+fp8rl_status check_attn_rows(const void* p, int64_t ld, int64_t n) {
+  if (!p) return FP8RL_ERR_NULL;
+  return ld >= kMaxPitch ? FP8RL_ERR_SHAPE : check_rows(p, ld, n);
+}
+
+// What both passes read (and fwd writes).
+fp8rl_status check_attn_inputs(const fp8rl_attn_args& a) {
+  const int64_t qc = (int64_t)a.q_heads * a.head_dim, kc = (int64_t)a.kv_heads * a.head_dim;
+  if (!a.q_offsets || !a.k_offsets) return FP8RL_ERR_NULL;
+  if (fp8rl_status s = check_attn_rows(a.q, a.ld_q, qc)) return s;
+  if (fp8rl_status s = check_attn_rows(a.out, a.ld_out, qc)) return s;
+  if (a.Tk > 0) {
+    if (fp8rl_status s = check_attn_rows(a.k, a.ld_k, kc)) return s;
+    if (fp8rl_status s = check_attn_rows(a.v, a.ld_v, kc)) return s;
+  }
+  if (!aligned(a.q_offsets, 4) || !aligned(a.k_offsets, 4) || !aligned(a.prefix, 4) ||
+      !aligned(a.slopes, 4) || !aligned(a.lse, 4))
+    return FP8RL_ERR_ALIGN;
+  return FP8RL_OK;
+}
+
+}  // namespace
+
+fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream) {
+  if (!args) return FP8RL_ERR_NULL;
+  const fp8rl_attn_args& a = *args;
+  if (fp8rl_status s = check_attn_shape(a)) return s;
+  if (a.Tq == 0 || a.docs == 0) return FP8RL_OK;
+  if (fp8rl_status s = check_attn_inputs(a)) return s;
+  return hip_status(fp8rl::launch_attn_fwd(a, as_stream(stream)));
+}
+
+size_t fp8rl_attn_bwd_workspace_bytes(int64_t Tq, int32_t q_heads) {
+  if (Tq < 0 || Tq >= (int64_t{1} << 24) || q_heads < 1 || q_heads > 4096) return 0;
+  return (size_t)Tq * (size_t)q_heads * sizeof(float);
+}
+
+fp8rl_status fp8rl_attn_bwd(const fp8rl_attn_args* args, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  if (!args) return FP8RL_ERR_NULL;
+  const fp8rl_attn_args& a = *args;
+  if (fp8rl_status s = check_attn_shape(a)) return s;
+  if ((a.Tq == 0 && a.Tk == 0) || a.docs == 0) return FP8RL_OK;
+  const int64_t qc = (int64_t)a.q_heads * a.head_dim, kc = (int64_t)a.kv_heads * a.head_dim;
+  if (!a.q_offsets || !a.k_offsets) return FP8RL_ERR_NULL;
+  if (a.Tq > 0) {
+    if (fp8rl_status s = check_attn_inputs(a)) return s;
+    if (!a.lse) return FP8RL_ERR_NULL;
+    if (fp8rl_status s = check_attn_rows(a.dout, a.ld_dout, qc)) return s;
+    if (fp8rl_status s = check_attn_rows(a.dq, a.ld_dq, qc)) return s;
+  }
+  if (a.Tk > 0) {
+    if (fp8rl_status s = check_attn_rows(a.k, a.ld_k, kc)) return s;
+    if (fp8rl_status s = check_attn_rows(a.v, a.ld_v, kc)) return s;
+    if (fp8rl_status s = check_attn_rows(a.dk, a.ld_dk, kc)) return s;
+    if (fp8rl_status s = check_attn_rows(a.dv, a.ld_dv, kc)) return s;
+  }
+  if (!aligned(a.q_offsets, 4) || !aligned(a.k_offsets, 4)) return FP8RL_ERR_ALIGN;
+  const size_t need = fp8rl_attn_bwd_workspace_bytes(a.Tq, a.q_heads);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return FP8RL_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return FP8RL_ERR_ALIGN;
+  }
+  return hip_status(fp8rl::launch_attn_bwd(a, (float*)workspace, as_stream(stream)));
+}
+
 }  // extern "C"

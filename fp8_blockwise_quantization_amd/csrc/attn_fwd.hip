@@ -1,0 +1,192 @@
+// Attention of packed documents.
+//
+// A workgroup has 128 queries of one head of a document, 32 a wave, and goes through the 64-key tiles that
+// any of them sees; keys and values reach LDS two tiles deep by direct loads. Per tile, with the
+// queries in the columns of the matrix instruction:
+//   S^T = K Q^T,   m = max(m, max S),   P = exp(S - m),   l += sum P,   O^T += V^T P^T,
+// so that a query's statistics are in the two lanes that hold its column, and P^T goes from one
+// product into the other in its registers (attn_tile.hpp). V^T is read out of V's rows by
+// the LDS's transposing read. m is raised, and O scaled, only where a maximum is more than 2^8
+// above it (P up to 2^8 loses nothing in float32 sums and bf16 operands).
+#include "attn_tile.hpp"
+
+namespace fp8rl {
+
+namespace {
+
+constexpr int kQ = 128, kK = 64, kWaves = 4;
+constexpr float kRise = 8.f;
+
+}  // namespace
+
+// DP: head_dim rounded up to 64 or 128; PAD: it is less. MORE: capped scores or slopes.
+template <int DP, bool PAD, bool MORE>
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
+  constexpr int KS = DP / 16, DT = DP / 32;
+  __shared__ __align__(1024) uint8_t s_k[2][kK * DP * 2];
+  __shared__ __align__(1024) uint8_t s_v[2][kK * DP * 2];
+  const fp8rl_attn_args& a = d.a;
+  const int lane = (int)(threadIdx.x & 63), h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int D = PAD ? a.head_dim : DP;
+
+  // key heads fastest (with 8 of them, one to an XCD and its L2), the last tiles of documents, which
+  // see the most keys, first
+  const int id = (int)blockIdx.x;
+  const int kv = id % a.kv_heads;
+  const int head = kv * d.group + id / a.kv_heads % d.group;
+  const DocTile t = find_tile<kQ, false>(a, d.slots - 1 - id / a.q_heads, lane);
+  if (t.doc >= (int)a.docs) return;
+  const Mask mask(a, t);
+  const int shift = t.lk - t.lq;
+  const int row = t.first + 32 * wave + (lane & 31);
+  const int p = row + shift;
+  const int rows = min(32, t.lq - t.first - 32 * wave);  // of this wave
+  const int p0 = t.first + 32 * wave + shift, p1 = p0 + rows - 1;
+
+  bf16x8 q[KS];
+  {
+    const uint16_t* at = a.q + (t.q0 + min(row, t.lq - 1)) * a.ld_q + (int64_t)head * D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) q[s] = row_operand(at, s, h, D);
+  }
+
+  // tiles: those of the prefix, then those from the first query's window to the last one's end
+  const int first = t.first + shift, last = min(t.first + kQ, t.lq) - 1 + shift;
+  const int in_prefix = (mask.prefix + kK - 1) / kK;
+  const int begin = max(mask.lo(first) / kK, in_prefix);
+  const int tiles = in_prefix + max(0, (mask.hi(last) + kK - 1) / kK - begin);
+  auto key_of = [&](int i) { return kK * (i < in_prefix ? i : i - in_prefix + begin); };
+
+  const RowLoader<DP, kK, kWaves> load_k(a.ld_k, D, wave, lane), load_v(a.ld_v, D, wave, lane);
+  const uint16_t* const k0 = a.k + t.k0 * a.ld_k + (int64_t)kv * D;
+  const uint16_t* const v0 = a.v + t.k0 * a.ld_v + (int64_t)kv * D;
+  auto load = [&](int i) {
+    const int j = key_of(i);
+    load_k.load(k0 + j * a.ld_k, t.lk - j, s_k[i & 1], wave);
+    load_v.load(v0 + j * a.ld_v, t.lk - j, s_v[i & 1], wave);
+  };
+
+  const bool capped = MORE && a.cap > 0.f, sloped = MORE && a.slopes;
+  const float slope2 = sloped ? a.slopes[head] * kLog2e : 0.f;
+  const float scale2 = MORE ? 1.f : d.scale2;  // what brings a score to units of ln 2
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) o[i] = zeros16();
+  float m = -__builtin_inff(), l = 0.f;
+
+  if (tiles > 0) load(0);
+  for (int i = 0; i < tiles; ++i) {
+    landed();
+    if (i + 1 < tiles) load(i + 1);
+    const int j0 = key_of(i), keys = min(kK, t.lk - j0);
+    if (keys < kK) {
+      clear_rows<DP, kK, kWaves>(s_v[i & 1], keys);
+      __syncthreads();
+    }
+    if (rows <= 0 || !mask.any(p0, p1, j0, j0 + keys)) continue;
+
+    const RowOperand<DP> kop(s_k[i & 1], lane);
+    f32x16 s[2] = {zeros16(), zeros16()};
+#pragma unroll
+    for (int c = 0; c < KS; ++c) {
+      if (PAD && 16 * c >= D) break;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        s[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kop(32 * r, c), q[c], s[r], 0, 0, 0);
+    }
+    if (MORE) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float x = s[r][e] * d.scale2;
+          if (capped) x = d.cap2 * tanh_cap(x);
+          const int j = j0 + 32 * r + 8 * (e >> 2) + 4 * h + (e & 3);
+          if (sloped) x -= slope2 * fabsf((float)(p - j));
+          s[r][e] = x;
+        }
+    }
+    if (keys < kK || !mask.all(p0, p1, j0, j0 + kK)) {
+      const int lo = mask.lo(p), hi = mask.hi(p);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = j0 + 32 * r + 8 * (e >> 2) + 4 * h + (e & 3);
+          s[r][e] = j < mask.prefix || (j >= lo && j < hi) ? s[r][e] : -__builtin_inff();
+        }
+    }
+    float top = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+    for (int e = 1; e < 16; ++e) top = fmaxf(fmaxf(top, s[0][e]), s[1][e]);
+    {
+      const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top),
+                                                      false, false);
+      top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * scale2;
+    }
+    if (__any(top > m + kRise)) {
+      const float was = m;
+      m = fmaxf(m, top);
+      const float f = m == -__builtin_inff() ? 1.f : exp2_fast(was - m);
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < DT; ++c) o[c] *= f;
+    }
+    const float ref = m == -__builtin_inff() ? 0.f : m;
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[r][e] = exp2_fast(__builtin_fmaf(s[r][e], scale2, -ref));
+        sum += s[r][e];
+      }
+    l += sum;
+
+    const ColOperand<DP> vop(s_v[i & 1], lane);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bf16x8 w = operand_of(s[r >> 1], r & 1);
+#pragma unroll
+      for (int c = 0; c < DT; ++c) {
+        if (PAD && 32 * c >= D) break;
+        o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vop(16 * r, c), w, o[c], 0, 0, 0);
+      }
+    }
+  }
+
+  if (rows <= 0) return;
+  {
+    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false,
+                                                    false);
+    l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  }
+  const bool in = row < t.lq;
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* const out = a.out + (t.q0 + row) * a.ld_out + (int64_t)head * D;
+#pragma unroll
+  for (int c = 0; c < DT; ++c) store_columns(o[c], f, out, 32 * c, h, D, in);
+  if (a.lse && in && h == 0)
+    a.lse[head * a.Tq + t.q0 + row] =
+        l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+}
+
+hipError_t launch_attn_fwd(const fp8rl_attn_args& a, hipStream_t stream) {
+  const AttnArgs d = attn_args(a, kQ, a.Tq);
+  const dim3 grid((unsigned)(d.slots * a.q_heads)), block(64 * kWaves);
+  const bool more = a.cap > 0.f || a.slopes;
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, d); };
+  if (a.head_dim == 64)
+    more ? go(attn_fwd_kernel<64, false, true>) : go(attn_fwd_kernel<64, false, false>);
+  else if (a.head_dim < 64)
+    more ? go(attn_fwd_kernel<64, true, true>) : go(attn_fwd_kernel<64, true, false>);
+  else if (a.head_dim < 128)
+    more ? go(attn_fwd_kernel<128, true, true>) : go(attn_fwd_kernel<128, true, false>);
+  else
+    more ? go(attn_fwd_kernel<128, false, true>) : go(attn_fwd_kernel<128, false, false>);
+  return hipGetLastError();
+}
+
+}  // namespace fp8rl

@@ -16,6 +16,12 @@ size_t attn_decode_workspace(int64_t B, int q_heads, int kv_heads, int head_dim,
                              int window);
 hipError_t launch_attn_decode(const fp8rl_attn_decode_args& a, void* workspace, hipStream_t stream);
 
+// ---- attn_fwd.hip
+hipError_t launch_attn_fwd(const fp8rl_attn_args& a, hipStream_t stream);
+
+// ---- attn_bwd.hip
+hipError_t launch_attn_bwd(const fp8rl_attn_args& a, float* delta, hipStream_t stream);
+
 // ---- kv_read.hip
 hipError_t launch_kv_read(const fp8rl_kv_read_args& a, hipStream_t stream);
 
@@ -74,18 +80,18 @@ struct PageOf {
   }
 };
 
-// The number of a row's document: how many of offsets[1 .. n] (not decreasing) are <= row, which is
-// the same in all lanes; n at most. 64 samples a step.
-__device__ __forceinline__ int document_of(const int32_t* offsets, int n, int row, int lane) {
-  int lo = 0, hi = n;  // offsets[lo] <= row (by convention for 0) and the answer is in [lo, hi]
+// The largest i <= n with at(i) <= x, at not decreasing (0 if there is none); x the same in all
+// lanes. 64 samples a step.
+template <typename F>
+__device__ __forceinline__ int last_not_past(int n, int x, int lane, F at) {
+  int lo = 0, hi = n;
   while (hi > lo) {
     const int step = (hi - lo + 63) >> 6;
-    const int at = lo + (lane + 1) * step;
-    const bool below = at <= hi && offsets[at] <= row;
-    lo += __popcll(__ballot(below)) * step;  // the last sample that is not past the row
+    const int i = lo + (lane + 1) * step;
+    lo += __popcll(__ballot(i <= hi && at(i) <= x)) * step;
     hi = min(hi, lo + step - 1);
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 }  // namespace fp8rl

@@ -30,7 +30,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs r) {
 
   int64_t from = -1;  // lane i: the cache row that row0 + i is a copy of
   {
-    int b = document_of(a.offsets, (int)a.B, row0, lane);
+    int b = last_not_past((int)a.B, row0, lane, [&](int i) { return a.offsets[i]; });
     const int row = row0 + lane;
     if (lane < kRows && row < a.R) {
       while (b < (int)a.B && a.offsets[b + 1] <= row) ++b;

@@ -481,6 +481,71 @@ int kv_read(PyObject* const* a) {
   return status;
 }
 
+// What both passes over packed documents are given: q, k, v, head_dim, q_offsets, k_offsets, causal,
+// sm_scale, window, prefix, cap, slopes, out, lse.
+fp8rl_attn_args attention(PyObject* const* a, int dev) {
+  fp8rl_attn_args r{};
+  const at::Tensor &q = tensor(a[0], "q", dev), &k = tensor(a[1], "k", dev),
+                   &out = tensor(a[12], "out", dev), &offsets = tensor(a[4], "q_offsets", dev);
+  need_2d(q, "q");
+  need_2d(k, "k");
+  const int64_t qc = q.size(1), kc = k.size(1);
+  r.Tq = q.size(0), r.Tk = k.size(0);
+  r.head_dim = int32_of(a[3], "head_dim");
+  r.q_heads = heads_in(qc, r.head_dim, "q"), r.kv_heads = heads_in(kc, r.head_dim, "k");
+  const Rows rq = matrix(q, "q", kBf16, r.Tq, qc), rk = matrix(k, "k", kBf16, r.Tk, kc),
+             rv = matrix(tensor(a[2], "v", dev), "v", kBf16, r.Tk, kc),
+             ro = matrix(out, "out", kBf16, r.Tq, qc);
+  r.q = (uint16_t*)rq.p, r.ld_q = rq.ld, r.k = (uint16_t*)rk.p, r.ld_k = rk.ld;
+  r.v = (uint16_t*)rv.p, r.ld_v = rv.ld, r.out = (uint16_t*)ro.p, r.ld_out = ro.ld;
+  if (offsets.numel() < 1) raise(PyExc_ValueError, "q_offsets needs at least one value");
+  r.docs = offsets.numel() - 1;
+  r.q_offsets = flat<int32_t>(a[4], "q_offsets", dev, at::kInt, r.docs + 1);
+  r.k_offsets = none(a[5]) ? r.q_offsets
+                           : flat<int32_t>(a[5], "k_offsets", dev, at::kInt, r.docs + 1);
+  const int causal = PyObject_IsTrue(a[6]);
+  if (causal < 0) throw Raised{};
+  r.causal = causal;
+  r.sm_scale = number(a[7]), r.window = int32_of(a[8], "window");
+  r.prefix = flat<int32_t>(a[9], "prefix", dev, at::kInt, r.docs);
+  r.cap = number(a[10]);
+  r.slopes = flat<float>(a[11], "slopes", dev, at::kFloat, r.q_heads);
+  r.lse = dense<float>(a[13], "lse", dev, at::kFloat, r.q_heads, r.Tq);
+  return r;
+}
+
+// those of attention(), dev, stream
+int attn_fwd(PyObject* const* a) {
+  const fp8rl_attn_args r = attention(a, (int)integer(a[14]));
+  void* stream = stream_of(a[15]);
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = fp8rl_attn_fwd(&r, stream);
+  Py_END_ALLOW_THREADS
+  return status;
+}
+
+// those of attention(), dout, dq, dk, dv, workspace, dev, stream
+int attn_bwd(PyObject* const* a) {
+  const int dev = (int)integer(a[19]);
+  fp8rl_attn_args r = attention(a, dev);
+  const int64_t qc = (int64_t)r.q_heads * r.head_dim, kc = (int64_t)r.kv_heads * r.head_dim;
+  const at::Tensor& dout = tensor(a[14], "dout", dev);
+  const Rows rg = matrix(dout, "dout", kBf16, r.Tq, qc),
+             rq = matrix(tensor(a[15], "dq", dev), "dq", kBf16, r.Tq, qc),
+             rk = matrix(tensor(a[16], "dk", dev), "dk", kBf16, r.Tk, kc),
+             rv = matrix(tensor(a[17], "dv", dev), "dv", kBf16, r.Tk, kc);
+  r.dout = (uint16_t*)rg.p, r.ld_dout = rg.ld, r.dq = (uint16_t*)rq.p, r.ld_dq = rq.ld;
+  r.dk = (uint16_t*)rk.p, r.ld_dk = rk.ld, r.dv = (uint16_t*)rv.p, r.ld_dv = rv.ld;
+  const Workspace ws(a[18], fp8rl_attn_bwd_workspace_bytes(r.Tq, r.q_heads), dout, dev);
+  void* stream = stream_of(a[20]);
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = fp8rl_attn_bwd(&r, ws.p, ws.bytes, stream);
+  Py_END_ALLOW_THREADS
+  return status;
+}
+
 // A function of N arguments as a Python callable: its status, or NULL with the exception set.
 template <int (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -510,6 +575,8 @@ PyMethodDef kMethods[] = {FP8RL_CALL(add_rmsnorm_quant, 11),
                           FP8RL_CALL(rope_kv_append, 18),
                           FP8RL_CALL(attn_decode, 16),
                           FP8RL_CALL(kv_read, 11),
+                          FP8RL_CALL(attn_fwd, 16),
+                          FP8RL_CALL(attn_bwd, 21),
                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods,

@@ -7,13 +7,15 @@
  *
  *   serving     one new token of every sequence against the paged cache that fp8rl_rope_kv_append
  *               fills (fp8rl_attn_decode), and cached rows back as contiguous bf16 rows
- *               (fp8rl_kv_read), the prefix in front of a chunk of prompt.
+ *               (fp8rl_kv_read), the prefix in front of a chunk of prompt;
+ *   documents   packed queries against packed keys (fp8rl_attn_fwd), prompts as well as training,
+ *               and the gradients (fp8rl_attn_bwd).
  *
  * Heads. Rows hold their heads side by side, head_dim columns each; kv_heads divides q_heads, and
  * q head h reads key head h / (q_heads / kv_heads).
  *
  * Which keys a query sees. A query at position p of its sequence sees key j of that sequence if
- *   j <= p and (window == 0 or p - j < window).
+ *   (not causal or j <= p) and (window == 0 or p - j < window),   or if   j < prefix.
  * Its score for such a key is, with s = sm_scale <q, k>,
  *   a = c - slopes[h] |p - j|,     c = cap tanh(s / cap)   (s itself with cap == 0),
  * without the slopes' term where slopes is NULL, and out = sum_j softmax(a)_j v_j. A query that sees
@@ -116,6 +118,72 @@ typedef struct {
  * and >= the columns. R == 0 or B == 0 returns FP8RL_OK.
  */
 fp8rl_status fp8rl_kv_read(const fp8rl_kv_read_args* args, void* stream);
+
+/* Arguments of fp8rl_attn_fwd and fp8rl_attn_bwd (a HOST struct, read during the call only). */
+typedef struct {
+  const uint16_t* q; /* bf16 [Tq][ld_q]: q_heads * head_dim columns */
+  const uint16_t* k; /* bf16 [Tk][ld_k]: kv_heads * head_dim columns */
+  const uint16_t* v; /* bf16 [Tk][ld_v] */
+  int64_t ld_q, ld_k, ld_v;
+  int64_t Tq, Tk;
+  int32_t q_heads, kv_heads, head_dim;
+  int64_t docs;
+  const int32_t* q_offsets; /* [docs + 1], not decreasing: document d's queries are rows
+                               q_offsets[d] .. q_offsets[d + 1] - 1 of q */
+  const int32_t* k_offsets; /* [docs + 1]: its keys' rows of k and v */
+  int32_t causal;
+  int32_t window;         /* 0: none */
+  const int32_t* prefix;  /* [docs], or NULL (none) */
+  float sm_scale;
+  float cap;              /* 0: none */
+  const float* slopes;    /* [q_heads] float32, or NULL */
+  uint16_t* out;          /* bf16 [Tq][ld_out]; written by fwd, read by bwd */
+  int64_t ld_out;
+  float* lse;             /* float32 [q_heads][Tq]: log sum_j exp(a_j), -inf where no key is seen;
+                             written by fwd (NULL: not), read by bwd */
+  const uint16_t* dout;   /* bf16 [Tq][ld_dout]: the gradient at out (bwd) */
+  int64_t ld_dout;
+  uint16_t* dq;           /* bf16 [Tq][ld_dq] (bwd) */
+  uint16_t* dk;           /* bf16 [Tk][ld_dk] */
+  uint16_t* dv;           /* bf16 [Tk][ld_dv] */
+  int64_t ld_dq, ld_dk, ld_dv;
+} fp8rl_attn_args;
+
+/*
+ * Attention of packed documents. With Lq queries and Lk keys, query i of a document is at position
+ * p = i + Lk - Lq: the keys of a chunk of prompt may begin with those of the prefix that is cached
+ * already. Rows that belong to no document are neither read nor written. Offsets outside [0, Tq] or
+ * [0, Tk] count as the nearest bound.
+ * Scores, statistics and sums are float32; the weights are rounded to bf16 for their product with v;
+ * out is rounded once. Deterministic.
+ * Values of v that are NaN or infinite reach rows of their document that do not see them (as 0 * NaN
+ * does); they reach no other document.
+ * Requires head_dim % 16 == 0, 16 <= head_dim <= 128, 1 <= kv_heads, q_heads a multiple of kv_heads,
+ * q_heads <= 4096, Tq, Tk < 2^24, docs < 2^20, sm_scale finite and > 0, window >= 0, cap finite and >= 0;
+ * 16-byte aligned rows, pitches multiples of 8 and >= the columns, offsets, prefix, lse and slopes
+ * 4-byte aligned. (max(Tq, Tk) / 128 + docs) * q_heads < 2^24, pitches < 2^24.
+ * Tq == 0 or docs == 0 returns FP8RL_OK.
+ */
+fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream);
+
+/*
+ * Gradients of fp8rl_attn_fwd. With P = exp(a - lse), dP = <dout, v> and D = <dout, out>:
+ *   dv_j = sum P dout,   dS = P (dP - D) (1 - (c / cap)^2),   dq_i = sm_scale sum_j dS k_j,
+ *   dk_j = sm_scale sum dS q,
+ * the sums for keys taken over the queries of all heads that share them. sm_scale, cap and slopes
+ * are constants. Rows of dq, dk and dv that belong to no document are not written; keys that no query
+ * sees get zeros. P and dS are rounded to bf16 for their products; sums are float32; each result is
+ * rounded once. Deterministic: no atomics. Values of q, k, v and dout that are NaN or infinite reach
+ * any row of their document, and no other document. Requires what fp8rl_attn_fwd does.
+ *   workspace : at least fp8rl_attn_bwd_workspace_bytes(Tq, q_heads) bytes, 16-byte aligned,
+ *               overwritten
+ * dq, dk and dv must not overlap the inputs or each other (columns of one fused row are fine).
+ */
+fp8rl_status fp8rl_attn_bwd(const fp8rl_attn_args* args, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Bytes of workspace fp8rl_attn_bwd needs. Host-only. */
+size_t fp8rl_attn_bwd_workspace_bytes(int64_t Tq, int32_t q_heads);
 
 #ifdef __cplusplus
 }

@@ -59,9 +59,9 @@ def gradients(q, k, v, dout, p, j, *, sm_scale, causal=True, window=0, prefix=0,
     dw = dout @ v.T
     mean = (w * dw).sum(axis=1, keepdims=True)
     ds = np.where(ok, sm_scale * w * (dw - mean) * slant, 0.0)
-    # what ds is formed of: both terms' magnitudes, before they cancel
+    # what ds is formed of: both terms' magnitudes, before they cancel and before the cap's slope
     big = w * ((np.abs(dout) @ np.abs(v).T) + (w @ np.abs(v) * np.abs(dout)).sum(1, keepdims=True))
-    big = np.where(ok, abs(sm_scale) * big * slant, 0.0)
+    big = np.where(ok, abs(sm_scale) * big, 0.0)
     return ((ds @ k, ds.T @ q, w.T @ dout),
             (big @ np.abs(k), big.T @ np.abs(q), w.T @ np.abs(dout)))
 

@@ -16,7 +16,8 @@ from fp8_blockwise_quantization_amd import _attn, _block, _lib
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "fp8rl_attn.h")
-STRUCTS = {"fp8rl_attn_decode_args": _attn.AttnDecodeArgs, "fp8rl_kv_read_args": _attn.KvReadArgs}
+STRUCTS = {"fp8rl_attn_decode_args": _attn.AttnDecodeArgs, "fp8rl_kv_read_args": _attn.KvReadArgs,
+           "fp8rl_attn_args": _attn.AttnArgs}
 
 OK, ENULL, ESHAPE, EALIGN, EDTYPE, EWS, EHIP, EARG, ESCRATCH = range(9)
 A = 1 << 20  # a fake, 16-byte aligned "device address": never dereferenced by these calls
@@ -165,6 +166,75 @@ def test_read_refusals(L):
     assert call(B=1 << 20) == ESHAPE
 
 
+DOCS = dict(q=A, k=A, v=A, ld_q=512, ld_k=256, ld_v=256, Tq=100, Tk=120, q_heads=4, kv_heads=2,
+            head_dim=128, docs=3, q_offsets=A, k_offsets=A, causal=1, window=0, prefix=A, sm_scale=0.1,
+            cap=0.0, slopes=A, out=A, ld_out=512, lse=A, dout=A, ld_dout=512, dq=A, dk=A, dv=A,
+            ld_dq=512, ld_dk=256, ld_dv=256)
+
+
+def attention_refusals(call, names, pitches):
+    for n in names:
+        assert call(**{n: None}) == ENULL, n
+    for n in names:
+        if "offsets" not in n and n != "lse":
+            assert call(**{n: A + 8}) == EALIGN, n
+    for n in ("q_offsets", "k_offsets", "prefix", "slopes", "lse"):
+        assert call(**{n: A + 2}) == EALIGN, n
+    for n in pitches:
+        assert call(**{n: DOCS[n] - 8}) == ESHAPE, n
+        assert call(**{n: DOCS[n] + 4}) == EALIGN, n
+        assert call(**{n: 1 << 24}) == ESHAPE, n
+    for d in (0, 8, 40, 144):
+        assert call(head_dim=d) == ESHAPE, d
+    for h in (0, -4, 1, 3, 4098):
+        assert call(q_heads=h) == ESHAPE, h
+    assert call(kv_heads=0) == ESHAPE
+    for n in ("Tq", "Tk", "docs"):
+        assert call(**{n: -1}) == ESHAPE, n
+        assert call(**{n: 1 << 24}) == ESHAPE, n
+    assert call(docs=(1 << 20) - 1, q_heads=20, ld_q=2560, ld_out=2560,
+                ld_dout=2560, ld_dq=2560) == ESHAPE  # 2^24 tiles
+    assert call(causal=2) == EARG
+    for v in (NAN, INF, 0.0, -1.0):
+        assert call(sm_scale=v) == EARG, v
+    for v in (NAN, INF, -1.0):
+        assert call(cap=v) == EARG, v
+    assert call(window=-1) == EARG
+
+
+def test_fwd_refusals(L):
+    def call(**k):
+        return L.fp8rl_attn_fwd(ctypes.byref(_attn.AttnArgs(**dict(DOCS, **k))), None)
+
+    assert L.fp8rl_attn_fwd(None, None) == ENULL
+    assert call(Tq=0, q=None, out=None) == OK
+    assert call(docs=0, q_offsets=None) == OK
+    attention_refusals(call, ("q", "k", "v", "out", "q_offsets", "k_offsets"),
+                       ("ld_q", "ld_k", "ld_v", "ld_out"))
+
+
+def test_bwd_refusals(L):
+    need = L.fp8rl_attn_bwd_workspace_bytes(100, 4)
+    assert need == 100 * 4 * 4
+    for bad in ((-1, 4), (1 << 24, 4), (100, 0), (100, 4097)):
+        assert L.fp8rl_attn_bwd_workspace_bytes(*bad) == 0
+
+    def call(ws=A, wsb=1 << 40, **k):
+        return L.fp8rl_attn_bwd(ctypes.byref(_attn.AttnArgs(**dict(DOCS, **k))), ws, wsb, None)
+
+    assert L.fp8rl_attn_bwd(None, A, 0, None) == ENULL
+    assert call(Tq=0, Tk=0, q=None, k=None) == OK
+    assert call(docs=0, q_offsets=None) == OK
+    attention_refusals(call, ("q", "k", "v", "out", "q_offsets", "k_offsets", "lse", "dout", "dq", "dk",
+                              "dv"),
+                       ("ld_q", "ld_k", "ld_v", "ld_out", "ld_dout", "ld_dq", "ld_dk", "ld_dv"))
+    assert call(Tk=0, k=None, dk=None, dq=None) == ENULL
+    assert call(Tq=0, q=None, dq=None, dv=None) == ENULL
+    assert call(ws=None) == EWS
+    assert call(wsb=need - 1) == EWS
+    assert call(ws=A + 8) == EALIGN
+
+
 def test_marshalling_module_refuses_before_any_launch():
     m = _block._marshal()
     x = torch.zeros((2, 128), dtype=torch.bfloat16)
@@ -174,6 +244,10 @@ def test_marshalling_module_refuses_before_any_launch():
         m.attn_decode(x, *[None] * 13, 0, 0)
     with pytest.raises(ValueError, match="page_table must be a device"):
         m.kv_read(*[x] * 9, 0, 0)
+    with pytest.raises(ValueError, match="q must be a device"):
+        m.attn_fwd(*[x] * 14, 0, 0)
+    with pytest.raises(ValueError, match="q must be a device"):
+        m.attn_bwd(*[x] * 19, 0, 0)
 
 
 def test_python_binding_refuses_host_tensors():
@@ -184,3 +258,7 @@ def test_python_binding_refuses_host_tensors():
         fq.attn_decode(bf(2, 64), cache, cache, i32(2, 1), i32(2))
     with pytest.raises(ValueError):
         fq.kv_read(cache, cache, i32(2, 1), i32(3), rows=4)
+    with pytest.raises(ValueError):
+        fq.attn_fwd(bf(2, 64), bf(2, 64), bf(2, 64), 64, i32(2))
+    with pytest.raises(ValueError):
+        fq.attn_bwd(*[bf(2, 64)] * 5, torch.zeros(1, 2), 64, i32(2))

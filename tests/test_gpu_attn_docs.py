@@ -1,0 +1,325 @@
+"""GPU parity of attention of packed documents and of its gradients against oracle.attn.
+
+How far results may be off, with U = 2^-24 (half a step of float32), BF = 2^-8 (of bf16):
+* a score: da = D U size + 8 U (|a| + cap) + 3 U slope distance + 4 U |a| (as for the paged cache:
+  products, scaling, tanh, slopes, the exponent's argument);
+* a weight: 2 da + 12 U of itself, and BF for its product with v; sums of n terms n U, numerator and
+  denominator;
+* lse: da + 8 U (|lse| + |a|) + n U;
+* gradients are formed from an lse rounded to float32 (U |lse|) and an out rounded to bf16. A weight
+  is off by e = da + 2 U |lse| + 4 U; dv = sum P dout by e + BF + n U of the sum of its terms'
+  magnitudes. dS = P (dP - delta): dP is a sum of D products, delta one with out off by BF, dS is
+  rounded to bf16, the cap's slope is off by 32 U of 1: e + 2 BF + 2 D U + 32 U of both terms'
+  magnitudes, n U for the sums over rows; every result is rounded once, BF of its value.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_blockwise_quantization_amd as fq
+from oracle import attn as oa
+from tests.gpu_util import assert_within
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF = 2.0 ** -8
+NAN = float("nan")
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Docs:
+    """Packed documents of nq queries and nk keys; rows of none (before, behind) hold NaN. `fused`:
+    q, k and v are column slices of one matrix (nq == nk)."""
+
+    def __init__(self, nq, nk=None, Hq=4, Hkv=2, D=64, *, causal=True, window=0, prefix=None, cap=0.0,
+                 slopes=False, sm_scale=None, seed=0, before=3, behind=2, fused=False):
+        self.nq, self.nk, self.Hq, self.Hkv, self.D = nq, list(nk or nq), Hq, Hkv, D
+        self.Tq, self.Tk = sum(nq) + before + behind, sum(self.nk) + before + behind
+        self.oq = (before + np.concatenate([[0], np.cumsum(nq)])).astype(int)
+        self.ok = (before + np.concatenate([[0], np.cumsum(self.nk)])).astype(int)
+        g = torch.Generator().manual_seed(seed)
+
+        def rows(T, H, o):
+            t = torch.randn((T, H * D), generator=g).to(torch.bfloat16)
+            t[:o[0]] = t[o[-1]:] = NAN
+            return t
+
+        self.q, self.k, self.v = (rows(self.Tq, Hq, self.oq), rows(self.Tk, Hkv, self.ok),
+                                  rows(self.Tk, Hkv, self.ok))
+        self.dout = (0.1 * rows(self.Tq, Hq, self.oq).float()).to(torch.bfloat16)
+        if fused:
+            one = torch.cat([self.q, self.k, self.v], dim=1).cuda()
+            self.dev = one.split([Hq * D, Hkv * D, Hkv * D], dim=1)
+        else:
+            self.dev = self.q.cuda(), self.k.cuda(), self.v.cuda()
+        self.slopes = (2.0 ** -(8 * (torch.arange(Hq) + 1) / Hq)).float() if slopes else None
+        self.prefix = prefix
+        self.scale = D ** -0.5 if sm_scale is None else sm_scale
+        self.mask = dict(causal=causal, window=window, cap=cap)
+        self.args = dict(self.mask, k_offsets=i32(self.ok.tolist()), sm_scale=sm_scale,
+                         slopes=None if self.slopes is None else self.slopes.cuda(),
+                         prefix=None if prefix is None else i32(prefix))
+        self.q_offsets = i32(self.oq.tolist())
+
+    def fwd(self, **more):
+        return fq.attn_fwd(*self.dev, self.D, self.q_offsets, **{**self.args, **more})
+
+    def each(self):
+        """Every head of every document: slices, positions, and the oracle's arguments."""
+        for d, (n, m) in enumerate(zip(self.nq, self.nk)):
+            rq, rk = slice(self.oq[d], self.oq[d + 1]), slice(self.ok[d], self.ok[d + 1])
+            p, j = np.arange(n) + m - n, np.arange(m)
+            for h in range(self.Hq):
+                cq = slice(h * self.D, (h + 1) * self.D)
+                kv = h * self.Hkv // self.Hq
+                ck = slice(kv * self.D, (kv + 1) * self.D)
+                yield rq, rk, cq, ck, h, p, j, dict(
+                    self.mask, sm_scale=self.scale, prefix=0 if self.prefix is None else self.prefix[d],
+                    slope=0.0 if self.slopes is None else float(self.slopes[h]))
+
+    def score_error(self, a, size, args, n):
+        big = np.abs(a).max() if a.size else 0.0
+        return (self.D * U * (size.max() if size.size else 0.0) + 12 * U * big
+                + 8 * U * args["cap"] + 3 * U * args["slope"] * n), big
+
+    def solve(self):
+        """Oracle: (out, tolerance), (lse, tolerance) over all rows; NaN where no document is."""
+        out = np.full((self.Tq, self.Hq * self.D), NAN)
+        tol = np.zeros_like(out)
+        lse, ltol = np.full((self.Hq, self.Tq), NAN), np.zeros((self.Hq, self.Tq))
+        for rq, rk, cq, ck, h, p, j, args in self.each():
+            if not len(p):
+                continue
+            v = f64(self.v[rk, ck])
+            o, ls, w, ok, size, a = oa.attend(f64(self.q[rq, cq]), f64(self.k[rk, ck]), v, p, j, **args)
+            da, big = self.score_error(a, size, args, max(len(p), len(j)))
+            rel = 2 * da + 12 * U + BF + 2 * len(j) * U
+            out[rq, cq] = o
+            tol[rq, cq] = BF * np.abs(o) + rel * (w @ np.abs(v)) + 1e-30
+            lse[h, rq] = ls
+            ltol[h, rq] = da + 8 * U * (np.where(np.isfinite(ls), np.abs(ls), 0) + big) + len(j) * U
+        return (out, tol), (lse, ltol)
+
+
+def check_fwd(d, **more):
+    out, lse = torch.full((d.Tq, d.Hq * d.D), 7.0, dtype=torch.bfloat16, device="cuda"), None
+    lse = torch.full((d.Hq, d.Tq), 7.0, device="cuda")
+    got, glse = d.fwd(out=out, lse=lse, **more)
+    assert got is out and glse is lse
+    (want, tol), (wlse, ltol) = d.solve()
+    live = ~np.isnan(want[:, 0])
+    assert (f64(out)[~live] == 7).all() and (f64(lse)[:, ~live] == 7).all()
+    assert_within(f64(out)[live], want[live], tol[live], "out")
+    g, w = f64(lse)[:, live], wlse[:, live]
+    some = np.isfinite(w)
+    assert (g[~some] == -np.inf).all()
+    assert_within(g[some], w[some], ltol[:, live][some], "lse")
+    return out, lse
+
+
+def check_bwd(d):
+    (want, _), (wlse, _) = d.solve()
+    out = torch.from_numpy(want).to(torch.bfloat16).cuda()
+    lse = torch.from_numpy(wlse).float().cuda()
+    kind = dict(dtype=torch.bfloat16, device="cuda")
+    grads = [torch.full(t.shape, 7.0, **kind) for t in (d.q, d.k, d.v)]
+    got = fq.attn_bwd(d.dout.cuda(), *d.dev, out, lse, d.D, d.q_offsets, dq=grads[0], dk=grads[1],
+                      dv=grads[2], **d.args)
+    assert all(a is b for a, b in zip(got, grads))
+    ref = [np.full(t.shape, 7.0) for t in (d.q, d.k, d.v)]
+    tol = [np.zeros(t.shape) for t in ref]
+    for rq, rk, cq, ck, h, p, j, args in d.each():
+        q, k, v, do = f64(d.q[rq, cq]), f64(d.k[rk, ck]), f64(d.v[rk, ck]), f64(d.dout[rq, cq])
+        g, size = oa.gradients(q, k, v, do, p, j, **args)
+        a, _, terms = oa.scores(q, k, p, j, sm_scale=args["sm_scale"], cap=args["cap"],
+                                slope=args["slope"])
+        da, _ = d.score_error(a, terms, args, max(len(p), len(j)))
+        fl = wlse[h, rq][np.isfinite(wlse[h, rq])]
+        e = da + 2 * U * (np.abs(fl).max() if fl.size else 0) + 4 * U
+        first = h % (d.Hq // d.Hkv) == 0
+        rows = len(p) * (d.Hq // d.Hkv)
+        rel = {0: e + 2 * BF + 2 * d.D * U + 32 * U + len(j) * U,
+               1: e + 2 * BF + 2 * d.D * U + 32 * U + rows * U, 2: e + BF + rows * U}
+        for i, at in enumerate(((rq, cq), (rk, ck), (rk, ck))):
+            if i == 0 or first:
+                ref[i][at], tol[i][at] = 0.0, 1e-30
+            ref[i][at] += g[i]
+            tol[i][at] += rel[i] * size[i]
+    for i, name in enumerate(("dq", "dk", "dv")):
+        assert_within(f64(grads[i]), ref[i], tol[i] + BF * np.abs(ref[i]) * (tol[i] > 0), name)
+    return grads
+
+
+LENGTHS = [[1], [2, 1, 0, 3], [31, 32, 33], [63, 64, 65, 128], [129, 7, 260]]
+MASKS = [dict(causal=False), dict(window=1), dict(window=50), dict(window=1000),
+         dict(causal=False, window=40), dict(prefix=[0, 70, 500]), dict(prefix=[3, 64, 200], window=20),
+         dict(prefix=[-4, 1, 130], window=33, causal=False), dict(cap=2.0), dict(slopes=True),
+         dict(cap=20.0, slopes=True, window=90, prefix=[5, 0, 80]), dict(sm_scale=1.7)]
+
+
+@pytest.mark.parametrize("lens", LENGTHS)
+def test_lengths(lens):
+    d = Docs(lens, D=128, seed=1)
+    check_fwd(d)
+    check_bwd(d)
+
+
+@pytest.mark.parametrize("D", [16, 32, 48, 64, 80, 96, 112, 128])
+@pytest.mark.parametrize("more", [{}, dict(cap=3.0, slopes=True)])
+def test_head_widths(D, more):
+    d = Docs([77, 150], D=D, seed=D, **more)
+    check_fwd(d)
+    check_bwd(d)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (7, 1), (6, 2), (16, 8)])
+def test_groups(Hq, Hkv):
+    d = Docs([70, 140], Hq=Hq, Hkv=Hkv, seed=Hq, fused=True)
+    check_fwd(d)
+    check_bwd(d)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("more", MASKS)
+def test_masks(more, D):
+    d = Docs([65, 140, 300], D=D, Hq=2, Hkv=1, seed=5, **more)
+    check_fwd(d)
+    check_bwd(d)
+
+
+@pytest.mark.parametrize("more", MASKS[:7] + MASKS[10:11])
+def test_more_keys_than_queries(more):
+    """A chunk behind a prefix; the last document has no more keys than queries see none of."""
+    d = Docs([1, 70, 130], [200, 333, 131], D=64, Hq=2, Hkv=1, seed=6, **more)
+    check_fwd(d)
+    check_bwd(d)
+
+
+@pytest.mark.parametrize("more", [{}, dict(prefix=[2, 0, 1]), dict(window=3)])
+def test_fewer_keys_than_queries(more):
+    """The first queries stand before the first key: they see none, or the prefix alone."""
+    d = Docs([140, 9, 70], [5, 0, 69], D=64, Hq=2, Hkv=2, seed=7, **more)
+    check_fwd(d)
+    check_bwd(d)
+
+
+def test_long_window_and_prefix_far_apart():
+    d = Docs([700], D=64, Hq=1, Hkv=1, seed=8, window=65, prefix=[70])
+    check_fwd(d)
+    check_bwd(d)
+    d = Docs([600], [900], D=128, Hq=1, Hkv=1, seed=8, window=2 ** 31 - 1)
+    check_fwd(d)
+    check_bwd(d)
+
+
+def test_many_documents():
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 4, 400).tolist()
+    d = Docs(lens, D=16, Hq=2, Hkv=1, seed=9, before=0, behind=0)
+    check_fwd(d)
+    check_bwd(d)
+
+
+def test_a_large_score_range():
+    """Scores that rise by hundreds from tile to tile, and rows that one key takes alone."""
+    d = Docs([300], D=64, Hq=2, Hkv=1, seed=10)
+    d.k *= torch.linspace(0.1, 40, d.Tk)[:, None].to(torch.bfloat16)
+    d.dev = d.q.cuda(), d.k.cuda(), d.v.cuda()
+    check_fwd(d)
+    check_bwd(d)
+
+
+def test_offsets_out_of_range_stay_in_bounds():
+    """Bounds beyond the rows count as the last row, negative ones as the first."""
+    d = Docs([60, 40], D=64, before=0, behind=0, seed=11)
+    want = d.fwd()
+    bad = i32([-5, 60, 2 ** 31 - 1])
+    got = fq.attn_fwd(*d.dev, 64, bad, k_offsets=bad)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_no_documents_no_rows():
+    d = Docs([5], D=64, seed=12)
+    out = torch.full((d.Tq, d.Hq * 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    fq.attn_fwd(*d.dev, 64, i32([0]), out=out)
+    assert (out == 7).all()
+    e = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    o, lse = fq.attn_fwd(e, d.dev[1], d.dev[2], 64, i32([0, 0]), k_offsets=i32([0, 5]))
+    assert o.shape == (0, 256) and lse.shape == (4, 0)
+    dq, dk, dv = fq.attn_bwd(e, e, d.dev[1], d.dev[2], o, lse, 64, i32([0, 0]), k_offsets=i32([3, 8]))
+    assert (dk[3:8] == 0).all() and (dv[3:8] == 0).all()
+    none = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")
+    o, lse = fq.attn_fwd(d.dev[0][3:8], none, none, 64, i32([0, 5]), k_offsets=i32([0, 0]))
+    assert (o == 0).all() and (lse == -float("inf")).all()
+    dq, _, _ = fq.attn_bwd(o, d.dev[0][3:8], none, none, o, lse, 64, i32([0, 5]), k_offsets=i32([0, 0]))
+    assert (dq == 0).all()
+
+
+def test_documents_do_not_reach_each_other():
+    d = Docs([70, 70, 70], D=64, seed=13)
+    want, grads = d.fwd(), None
+    g0 = fq.attn_bwd(d.dout.cuda(), *d.dev, *want, 64, d.q_offsets, **d.args)
+    for t in d.dev:
+        t[d.oq[1]:d.oq[2]] = NAN
+    dout = d.dout.cuda()
+    dout[d.oq[1]:d.oq[2]] = NAN
+    got = d.fwd()
+    keep = np.r_[d.oq[0]:d.oq[1], d.oq[2]:d.oq[3]]
+    assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1][:, keep], want[1][:, keep])
+    assert got[0][d.oq[1]:d.oq[2]].isnan().all()
+    g1 = fq.attn_bwd(dout, *d.dev, *got, 64, d.q_offsets, **d.args)
+    for a, b in zip(g0, g1):
+        assert torch.equal(a[keep], b[keep])
+
+
+def test_gradients_as_columns_of_one_row():
+    d = Docs([90, 33], D=80, seed=14, fused=True)
+    out, lse = d.fwd()
+    want = fq.attn_bwd(d.dout.cuda(), *d.dev, out, lse, 80, d.q_offsets, **d.args)
+    one = torch.full((d.Tq, 8 * 80 + 16), 3.0, dtype=torch.bfloat16, device="cuda")
+    dq, dk, dv, rest = one.split([320, 160, 160, 16], dim=1)
+    fq.attn_bwd(d.dout.cuda(), *d.dev, out, lse, 80, d.q_offsets, dq=dq, dk=dk, dv=dv, **d.args)
+    rows = slice(d.oq[0], d.oq[-1])
+    for a, b in zip((dq, dk, dv), want):
+        assert torch.equal(a[rows], b[rows]) and (a[:3] == 3).all() and (a[d.oq[-1]:] == 3).all()
+    assert (rest == 3).all()
+
+
+def test_gradients_against_autograd_in_float64():
+    d = Docs([150], D=64, Hq=4, Hkv=2, seed=15, before=0, behind=0, cap=4.0)
+    q, k, v = (t.double().clone().requires_grad_() for t in (d.q, d.k, d.v))
+    heads = lambda t: t.view(150, -1, 64).transpose(0, 1)  # noqa: E731
+    s = heads(q) @ heads(k).repeat_interleave(2, 0).transpose(1, 2) / 8
+    s = 4 * torch.tanh(s / 4)
+    s = s.masked_fill(torch.ones(150, 150).triu(1).bool(), -torch.inf)
+    o = (s.softmax(-1) @ heads(v).repeat_interleave(2, 0)).transpose(0, 1).reshape(150, -1)
+    (o * d.dout.double()).sum().backward()
+    out, lse = d.fwd()
+    got = fq.attn_bwd(d.dout.cuda(), *d.dev, out, lse, 64, d.q_offsets, **d.args)
+    for a, b in zip(got, (q.grad, k.grad, v.grad)):
+        # the roundings of P, dS and out, BF each, over sums of at most 150 terms of mixed sign
+        assert (f64(a) - b.numpy()).std() < 3 * BF * b.numpy().std()
+
+
+def test_repeats():
+    d = Docs([300, 41], D=128, seed=16)
+    runs = [d.fwd() for _ in range(2)]
+    assert torch.equal(runs[0][0][3:-2], runs[1][0][3:-2])
+    g = []
+    need = fq.fp8rl_attn_bwd_workspace_bytes(d.Tq, d.Hq)
+    for fill in (0, 255):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        g.append(fq.attn_bwd(d.dout.cuda(), *d.dev, *runs[0], 128, d.q_offsets, workspace=ws, **d.args))
+    for a, b in zip(*g):
+        assert torch.equal(a[3:-2], b[3:-2])
+    with pytest.raises(fq.Fp8rlError):
+        fq.attn_bwd(d.dout.cuda(), *d.dev, *runs[0], 128, d.q_offsets, workspace=ws[:need - 4], **d.args)
