@@ -77,7 +77,7 @@ def declare_attn(L: ctypes.CDLL) -> ctypes.CDLL:
         "fp8rl_kv_read": (ci, [ptr(KvReadArgs), _P]),
         "fp8rl_attn_fwd": (ci, [ptr(AttnArgs), _P]),
         "fp8rl_attn_bwd": (ci, [ptr(AttnArgs), _P, sz, _P]),
-        "fp8rl_attn_bwd_workspace_bytes": (sz, [_I64, _I32]),
+        "fp8rl_attn_bwd_workspace_bytes": (sz, [_I64, _I64, _I64, _I32, _I32, _I32]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -190,8 +190,9 @@ def fp8rl_attn_fwd(q, k, v, head_dim: int, q_offsets, k_offsets=None, causal: bo
     return out, lse
 
 
-def fp8rl_attn_bwd_workspace_bytes(Tq: int, q_heads: int) -> int:
-    return int(_attn_lib().fp8rl_attn_bwd_workspace_bytes(Tq, q_heads))
+def fp8rl_attn_bwd_workspace_bytes(Tq: int, Tk: int, docs: int, q_heads: int, kv_heads: int,
+                                   head_dim: int) -> int:
+    return int(_attn_lib().fp8rl_attn_bwd_workspace_bytes(Tq, Tk, docs, q_heads, kv_heads, head_dim))
 
 
 def fp8rl_attn_bwd(dout, q, k, v, out, lse, head_dim: int, q_offsets, k_offsets=None,

@@ -158,13 +158,18 @@ namespace {
 
 constexpr int64_t kMaxPitch = int64_t{1} << 24;  // 64 rows are less than 2^32 bytes apart
 
+fp8rl_status check_attn_sizes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_heads, int32_t kv_heads,
+                              int32_t head_dim) {
+  if (Tq < 0 || Tk < 0 || Tq >= (int64_t{1} << 24) || Tk >= (int64_t{1} << 24)) return FP8RL_ERR_SHAPE;
+  if (docs < 0 || docs >= (int64_t{1} << 20)) return FP8RL_ERR_SHAPE;
+  if (fp8rl_status s = check_heads(q_heads, kv_heads, head_dim, 128)) return s;
+  if (((Tq > Tk ? Tq : Tk) / 128 + docs) * q_heads >= (int64_t{1} << 24)) return FP8RL_ERR_SHAPE;
+  return FP8RL_OK;
+}
+
 fp8rl_status check_attn_shape(const fp8rl_attn_args& a) {
-  if (a.Tq < 0 || a.Tk < 0 || a.Tq >= (int64_t{1} << 24) || a.Tk >= (int64_t{1} << 24))
-    return FP8RL_ERR_SHAPE;
-  if (a.docs < 0 || a.docs >= (int64_t{1} << 20)) return FP8RL_ERR_SHAPE;
-  if (fp8rl_status s = check_heads(a.q_heads, a.kv_heads, a.head_dim, 128)) return s;
-  if (((a.Tq > a.Tk ? a.Tq : a.Tk) / 128 + a.docs) * a.q_heads >= (int64_t{1} << 24))
-    return FP8RL_ERR_SHAPE;
+  if (fp8rl_status s = check_attn_sizes(a.Tq, a.Tk, a.docs, a.q_heads, a.kv_heads, a.head_dim))
+    return s;
   if (a.causal != 0 && a.causal != 1) return FP8RL_ERR_ARG;
   if (fp8rl_status s = check_scores(a.sm_scale, a.window, a.cap)) return s;
   return a.sm_scale > 0.f ? FP8RL_OK : FP8RL_ERR_ARG;
@@ -202,9 +207,10 @@ fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream) {
   return hip_status(fp8rl::launch_attn_fwd(a, as_stream(stream)));
 }
 
-size_t fp8rl_attn_bwd_workspace_bytes(int64_t Tq, int32_t q_heads) {
-  if (Tq < 0 || Tq >= (int64_t{1} << 24) || q_heads < 1 || q_heads > 4096) return 0;
-  return (size_t)Tq * (size_t)q_heads * sizeof(float);
+size_t fp8rl_attn_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_heads,
+                                      int32_t kv_heads, int32_t head_dim) {
+  if (check_attn_sizes(Tq, Tk, docs, q_heads, kv_heads, head_dim) != FP8RL_OK) return 0;
+  return fp8rl::attn_bwd_workspace(Tq, Tk, docs, q_heads, kv_heads, head_dim);
 }
 
 fp8rl_status fp8rl_attn_bwd(const fp8rl_attn_args* args, void* workspace, size_t workspace_bytes,
@@ -228,7 +234,8 @@ fp8rl_status fp8rl_attn_bwd(const fp8rl_attn_args* args, void* workspace, size_t
     if (fp8rl_status s = check_attn_rows(a.dv, a.ld_dv, kc)) return s;
   }
   if (!aligned(a.q_offsets, 4) || !aligned(a.k_offsets, 4)) return FP8RL_ERR_ALIGN;
-  const size_t need = fp8rl_attn_bwd_workspace_bytes(a.Tq, a.q_heads);
+  const size_t need =
+      fp8rl::attn_bwd_workspace(a.Tq, a.Tk, a.docs, a.q_heads, a.kv_heads, a.head_dim);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return FP8RL_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return FP8RL_ERR_ALIGN;

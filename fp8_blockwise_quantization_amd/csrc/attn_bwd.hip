@@ -5,11 +5,16 @@
 //
 // dq: as the forward pass, 128 queries a workgroup, queries in the columns. Per tile of 64 keys
 //   S^T = K Q^T,  dP^T = V dO^T,  P = exp(S - lse),  dS = P (dP - delta),  dQ^T += K^T dS^T,
-// where delta = <dout, out> of a query, formed first and left in the workspace for the second pass.
+// where delta = <dout, out> of a query, formed first and left in the workspace (with lse in units of ln 2)
+// for the second pass.
 //
 // dk, dv: 128 keys a workgroup, keys in the columns, through the tiles of 64 queries of all heads
 // that share the keys:
 //   S = Q K^T,  dP = dO V^T,  dV^T += dO^T P,  dK^T += Q^T dS.
+#include <limits.h>
+
+#include <type_traits>
+
 #include "attn_tile.hpp"
 
 namespace fp8rl {
@@ -18,7 +23,68 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kOwn = 128;   // rows of a workgroup
-constexpr int kPass = 64;   // rows of a tile that it goes through
+constexpr int kPass = 64;   // keys of a tile that the first pass goes through
+constexpr int kQueries = 64; // queries of a tile that the second goes through
+constexpr int kMostParts = 8;
+
+// The tiles of queries that see any of a workgroup's keys, those of the group's heads one after
+// another.
+struct QueryTiles {
+  int begin, per, total;  // of a head: begin .. begin + per - 1
+  __device__ __forceinline__ QueryTiles(const Mask& mask, const DocTile& t, int group) {
+    const int shift = t.lk - t.lq;
+    int first = 0, end = t.lq;
+    if (t.first >= mask.prefix) {
+      const int past = min(t.first + kOwn, t.lk);  // behind the last key
+      if (mask.causal) first = max(0, t.first - shift);
+      if (mask.window) end = min(t.lq, past + mask.window - 1 - shift);
+    }
+    begin = first / kQueries;
+    per = max(0, (end + kQueries - 1) / kQueries - begin);
+    total = per * group;
+  }
+  __device__ __forceinline__ int cut(int part, int parts) const {
+    return (int)((int64_t)total * part / parts);
+  }
+};
+
+// The exponent of a weight, in units of ln 2: the score of a product s at distance p - j, less lse. With
+// a cap, the slope of the capped score there.
+template <bool MORE>
+__device__ __forceinline__ float score(float s, const AttnArgs& d, bool capped, bool sloped,
+                                       float slope2, int distance, float lse2, float& slant) {
+  if (!MORE) return __builtin_fmaf(s, d.scale2, -lse2);
+  float x = s * d.scale2;
+  if (capped) {
+    const float th = tanh_cap(x);
+    x = d.cap2 * th;
+    slant = 1.f - th * th;
+  }
+  if (sloped) x -= slope2 * fabsf((float)distance);
+  return x - lse2;
+}
+
+// Where a wave's lane keeps its part of dk (and behind it dv) of the keys of workgroup `tile`.
+template <int DP>
+__device__ __forceinline__ f32x4* part_of(const AttnArgs& d, int tile, int part, int wave, int lane) {
+  return reinterpret_cast<f32x4*>(d.part) +
+         (((int64_t)tile * d.parts + part) * kWaves + wave) * (2 * 32 * DP / 4) + lane;
+}
+
+template <int DP>
+__device__ __forceinline__ void store_key_grads(const fp8rl_attn_args& a, const DocTile& t,
+                                                const f32x16 (&dk)[DP / 32],
+                                                const f32x16 (&dv)[DP / 32], int kv, int key, int h,
+                                                int D) {
+  const bool in = key < t.lk;
+  uint16_t* const ok = a.dk + (t.k0 + key) * a.ld_dk + (int64_t)kv * D;
+  uint16_t* const ov = a.dv + (t.k0 + key) * a.ld_dv + (int64_t)kv * D;
+#pragma unroll
+  for (int c = 0; c < DP / 32; ++c) {
+    store_columns(dk[c], a.sm_scale, ok, 32 * c, h, D, in);
+    store_columns(dv[c], 1.f, ov, 32 * c, h, D, in);
+  }
+}
 
 }  // namespace
 
@@ -65,11 +131,14 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
     const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(delta), __float_as_uint(delta),
                                                     false, false);
     delta = __uint_as_float(x[0]) + __uint_as_float(x[1]);
-    if (in && h == 0) d.delta[head * a.Tq + qrow] = delta;
   }
   // a query that sees nothing: exp(S - inf) = 0 throughout
   float lse2 = a.lse[head * a.Tq + qrow] * kLog2e;
   if (lse2 == -__builtin_inff()) lse2 = __builtin_inff();
+  if (in && h == 0) {
+    d.stats[head * a.Tq + qrow] = lse2;
+    d.stats[(a.q_heads + head) * a.Tq + qrow] = delta;
+  }
 
   const int first = t.first + shift, last = min(t.first + kOwn, t.lq) - 1 + shift;
   const int in_prefix = (mask.prefix + kPass - 1) / kPass;
@@ -77,13 +146,13 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
   const int tiles = in_prefix + max(0, (mask.hi(last) + kPass - 1) / kPass - begin);
   auto key_of = [&](int i) { return kPass * (i < in_prefix ? i : i - in_prefix + begin); };
 
-  const RowLoader<DP, kPass, kWaves> load_k(a.ld_k, D, wave, lane), load_v(a.ld_v, D, wave, lane);
+  const RowLoader<DP, kPass, kWaves> rows_in(D, wave, lane);
   const uint16_t* const k0 = a.k + t.k0 * a.ld_k + (int64_t)kv * D;
   const uint16_t* const v0 = a.v + t.k0 * a.ld_v + (int64_t)kv * D;
   auto load = [&](int i) {
     const int j = key_of(i);
-    load_k.load(k0 + j * a.ld_k, t.lk - j, s_k[i & 1], wave);
-    load_v.load(v0 + j * a.ld_v, t.lk - j, s_v[i & 1], wave);
+    rows_in.load(k0 + j * a.ld_k, a.ld_k, t.lk - j, s_k[i & 1], wave);
+    rows_in.load(v0 + j * a.ld_v, a.ld_v, t.lk - j, s_v[i & 1], wave);
   };
   const bool capped = MORE && a.cap > 0.f, sloped = MORE && a.slopes;
   const float slope2 = sloped ? a.slopes[head] * kLog2e : 0.f;
@@ -102,34 +171,36 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
       __syncthreads();
     }
     if (rows <= 0 || !mask.any(p0, p1, j0, j0 + keys)) continue;
-    const bool all = keys == kPass && mask.all(p0, p1, j0, j0 + kPass);
     const int lo = mask.lo(p), hi = mask.hi(p);
     const RowOperand<DP> kop(s_k[i & 1], lane), vop(s_v[i & 1], lane);
     const ColOperand<DP> kt(s_k[i & 1], lane);
+    f32x16 s, dp;
+    auto weigh = [&](int r, auto masked) {  // dS in its place
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int j = j0 + 32 * r + 8 * (e >> 2) + 4 * h + (e & 3);
+        float slant = 1.f;
+        const float x = score<MORE>(s[e], d, capped, sloped, slope2, p - j, lse2, slant);
+        float ds = exp2_fast(x) * (dp[e] - delta);
+        if (capped) ds *= slant;
+        if (masked) ds = (j < mask.prefix) | ((j >= lo) & (j < hi)) ? ds : 0.f;
+        s[e] = ds;
+      }
+    };
+    const bool all = keys == kPass && mask.all(p0, p1, j0, j0 + kPass);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {  // 32 keys
-      f32x16 s = zeros16(), dp = zeros16();
+      s = zeros16(), dp = zeros16();
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
         if (PAD && 16 * c >= D) break;
         s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kop(32 * r, c), q[c], s, 0, 0, 0);
         dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vop(32 * r, c), g[c], dp, 0, 0, 0);
       }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int j = j0 + 32 * r + 8 * (e >> 2) + 4 * h + (e & 3);
-        float x = s[e] * d.scale2, slant = 1.f;
-        if (capped) {
-          const float th = tanh_cap(x);
-          x = d.cap2 * th;
-          slant = 1.f - th * th;
-        }
-        if (sloped) x -= slope2 * fabsf((float)(p - j));
-        float ds = exp2_fast(x - lse2) * (dp[e] - delta);
-        if (capped) ds *= slant;
-        if (!all) ds = j < mask.prefix || (j >= lo && j < hi) ? ds : 0.f;
-        s[e] = ds;
-      }
+      if (all)
+        weigh(r, std::false_type{});
+      else
+        weigh(r, std::true_type{});
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const bf16x8 w = operand_of(s, u);
@@ -148,112 +219,134 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
 }
 
 template <int DP, bool PAD, bool MORE>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs d) {
+__global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnArgs d) {
   constexpr int KS = DP / 16, DT = DP / 32;
-  __shared__ __align__(1024) uint8_t s_q[2][kPass * DP * 2];
-  __shared__ __align__(1024) uint8_t s_g[2][kPass * DP * 2];
-  __shared__ __align__(1024) float s_row[2][2][kPass];  // lse and delta of the tile's queries
+  constexpr int kTile = kQueries * DP * 2;  // bytes
+  // q and dout of three tiles, and v; in the end the sums of half of the waves
+  __shared__ __align__(1024) uint8_t s_mem[6 * kTile + kOwn * DP * 2];
+  __shared__ __align__(1024) float s_row[3][2][kQueries];  // lse and delta of the tile's queries
+  // the steps of the keys' operand that do not fit the registers beside the sums (spilled, their
+  // reloads would wait for the tiles in flight)
+  constexpr int kHeld = DP == 64 ? KS : MORE && PAD ? KS - 6 : KS - 4;
+  __shared__ u32x4 s_k[4][KS - kHeld + 1][64];
+  uint8_t* const s_v = s_mem + 6 * kTile;
   const fp8rl_attn_args& a = d.a;
   const int lane = (int)(threadIdx.x & 63), h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int block = wave & 3, half = wave >> 2;  // of the keys, of a tile's queries
   const int D = PAD ? a.head_dim : DP;
 
   const int id = (int)blockIdx.x;
   const int kv = id % a.kv_heads;
-  const DocTile t = find_tile<kOwn, true>(a, id / a.kv_heads, lane);
+  const int part = id / a.kv_heads % d.parts;
+  const DocTile t = find_tile<kOwn, true>(a, id / (a.kv_heads * d.parts), lane);
   if (t.doc >= (int)a.docs) return;
   const Mask mask(a, t);
   const int shift = t.lk - t.lq;
-  const int key = t.first + 32 * wave + (lane & 31);
-  const int keys = min(32, t.lk - t.first - 32 * wave);  // of this wave
-  const int j0 = t.first + 32 * wave, j1 = j0 + keys;
+  const int j0 = t.first + 32 * block, key = j0 + (lane & 31);
+  const int keys = min(32, t.lk - j0), j1 = j0 + keys;  // of this wave
 
-  bf16x8 k[KS], v[KS];
-  {
-    const int64_t krow = t.k0 + min(key, t.lk - 1);
-    const uint16_t* kp = a.k + krow * a.ld_k + (int64_t)kv * D;
-    const uint16_t* vp = a.v + krow * a.ld_v + (int64_t)kv * D;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) k[s] = row_operand(kp, s, h, D), v[s] = row_operand(vp, s, h, D);
-  }
+  // the queries that see any of the workgroup's keys, in whole tiles, for each head of the group;
+  // of these tiles the workgroup's part
+  const QueryTiles all_tiles(mask, t, d.group);
+  const int from = all_tiles.cut(part, d.parts), tiles = all_tiles.cut(part + 1, d.parts) - from;
+  auto head_of = [&](int i) { return kv * d.group + (from + i) / all_tiles.per; };
+  auto row_of = [&](int i) { return kQueries * ((from + i) % all_tiles.per + all_tiles.begin); };
 
-  // the queries that see any of the workgroup's keys, in whole tiles, for each head of the group
-  int begin = 0, end = t.lq;
-  if (t.first >= mask.prefix) {
-    const int past = min(t.first + kOwn, t.lk);  // behind the last key
-    if (mask.causal) begin = max(0, t.first - shift);
-    if (mask.window) end = (int)min((int64_t)t.lq, (int64_t)past + mask.window - 1 - shift);
-  }
-  begin /= kPass;
-  const int per = max(0, (end + kPass - 1) / kPass - begin);
-  const int tiles = per * d.group;
-
-  const RowLoader<DP, kPass, kWaves> load_q(a.ld_q, D, wave, lane), load_g(a.ld_dout, D, wave, lane);
+  const RowLoader<DP, kQueries, 8> rows_in(D, wave, lane);
+  constexpr int kLoads = 2 * RowLoader<DP, kQueries, 8>::kOps + 1;
   auto load = [&](int i) {
-    const int in_group = i / per;
-    const int head = kv * d.group + in_group, r0 = kPass * (i - in_group * per + begin);
+    const int head = head_of(i), r0 = row_of(i), at = i % 3;
     const int64_t row = t.q0 + r0;
-    load_q.load(a.q + row * a.ld_q + (int64_t)head * D, t.lq - r0, s_q[i & 1], wave);
-    load_g.load(a.dout + row * a.ld_dout + (int64_t)head * D, t.lq - r0, s_g[i & 1], wave);
-    if (wave < 2)
-      dma_floats((wave == 0 ? a.lse : d.delta) + head * a.Tq + row,
-                 4 * (uint32_t)min(lane, t.lq - r0 - 1), s_row[i & 1][wave]);
+    rows_in.load(a.q + row * a.ld_q + (int64_t)head * D, a.ld_q, t.lq - r0, s_mem + 2 * at * kTile,
+                 wave);
+    rows_in.load(a.dout + row * a.ld_dout + (int64_t)head * D, a.ld_dout, t.lq - r0,
+                 s_mem + (2 * at + 1) * kTile, wave);
+    // (the even waves all load the same, and so do the odd ones: every wave has as many loads in
+    // flight)
+    dma_floats(d.stats + ((wave & 1) * a.q_heads + head) * a.Tq + row,
+               4 * (uint32_t)min(lane, t.lq - r0 - 1), s_row[at][wave & 1]);
   };
+
+  // the keys stay in registers, their values in LDS
+  RowLoader<DP, kOwn, 8>(D, wave, lane)
+      .load(a.v + (t.k0 + t.first) * a.ld_v + (int64_t)kv * D, a.ld_v, t.lk - t.first, s_v, wave);
+  if (tiles > 0) load(0);
+  bf16x8 k[kHeld];
+  {
+    const uint16_t* kp = a.k + (t.k0 + min(key, t.lk - 1)) * a.ld_k + (int64_t)kv * D;
+#pragma unroll
+    for (int s = 0; s < kHeld; ++s) k[s] = row_operand(kp, s, h, D);
+#pragma unroll
+    for (int s = kHeld; s < KS; ++s)
+      if (half == 0) s_k[block][s - kHeld][lane] = __builtin_bit_cast(u32x4, row_operand(kp, s, h, D));
+  }
   const bool capped = MORE && a.cap > 0.f, sloped = MORE && a.slopes;
+  const RowOperand<DP> vop(s_v + 32 * block * DP * 2, lane);
 
   f32x16 dk[DT], dv[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i) dk[i] = zeros16(), dv[i] = zeros16();
 
-  if (tiles > 0) load(0);
+  if (tiles > 1) load(1);
   for (int i = 0; i < tiles; ++i) {
-    landed();
-    if (i + 1 < tiles) load(i + 1);
-    const int in_group = i / per;
-    const int head = kv * d.group + in_group, r0 = kPass * (i - in_group * per + begin);
-    const int rows = min(kPass, t.lq - r0);
-    if (rows < kPass) {
-      clear_rows<DP, kPass, kWaves>(s_q[i & 1], rows);
-      clear_rows<DP, kPass, kWaves>(s_g[i & 1], rows);
+    if (i + 1 < tiles)
+      landed<kLoads>();
+    else
+      landed<0>();
+    if (i + 2 < tiles) load(i + 2);
+    uint8_t* const s_q = s_mem + 2 * (i % 3) * kTile;
+    uint8_t* const s_g = s_q + kTile;
+    const int r0 = row_of(i);
+    const int in_tile = min(kQueries, t.lq - r0);
+    if (in_tile < kQueries) {
+      clear_rows<DP, kQueries, 8>(s_q, in_tile);
+      clear_rows<DP, kQueries, 8>(s_g, in_tile);
       __syncthreads();
     }
-    const float slope2 = sloped ? a.slopes[head] * kLog2e : 0.f;
-    const RowOperand<DP> qop(s_q[i & 1], lane), gop(s_g[i & 1], lane);
-    const ColOperand<DP> qt(s_q[i & 1], lane), gt(s_g[i & 1], lane);
+    const int rows = min(32, in_tile - 32 * half);  // of this wave
+    const int p0 = r0 + 32 * half + shift;
+    if (keys <= 0 || rows <= 0 || !mask.any(p0, p0 + rows - 1, j0, j1)) continue;
+    const float slope2 = sloped ? a.slopes[head_of(i)] * kLog2e : 0.f;
+    const RowOperand<DP> qop(s_q + 32 * half * DP * 2, lane), gop(s_g + 32 * half * DP * 2, lane);
+    const ColOperand<DP> qt(s_q + 32 * half * DP * 2, lane), gt(s_g + 32 * half * DP * 2, lane);
+
+    f32x16 s = zeros16(), dp = zeros16();
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {  // 32 queries
-      const int n = min(32, rows - 32 * r);
-      const int p0 = r0 + 32 * r + shift;
-      if (keys <= 0 || n <= 0 || !mask.any(p0, p0 + n - 1, j0, j1)) continue;
-      const bool all = n == 32 && keys == 32 && mask.all(p0, p0 + 31, j0, j1);
-      f32x16 s = zeros16(), dp = zeros16();
+    for (int c = 0; c < KS; ++c) {
+      if (PAD && 16 * c >= D) break;
+      const bf16x8 kc =
+          c < kHeld ? k[c < kHeld ? c : 0] : __builtin_bit_cast(bf16x8, s_k[block][c - kHeld][lane]);
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qop(0, c), kc, s, 0, 0, 0);
+    }
 #pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        if (PAD && 16 * c >= D) break;
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qop(32 * r, c), k[c], s, 0, 0, 0);
-        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(gop(32 * r, c), v[c], dp, 0, 0, 0);
+    for (int c = 0; c < KS; ++c) {
+      if (PAD && 16 * c >= D) break;
+      dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(gop(0, c), vop(0, c), dp, 0, 0, 0);
+    }
+    auto weigh = [&](auto masked) {  // P and dS in their places
+      // the positions that see this lane's key: from <= p < to
+      int from = 0, to = 0;
+      if (masked) {
+        const bool prefixed = key < mask.prefix;
+        from = key >= t.lk ? INT_MAX : prefixed || !mask.causal ? INT_MIN : key;
+        to = min(p0 + rows, prefixed || !mask.window ? INT_MAX : key + mask.window);
       }
 #pragma unroll
       for (int e4 = 0; e4 < 4; ++e4) {
-        const f32x4 lse = *reinterpret_cast<const f32x4*>(&s_row[i & 1][0][32 * r + 8 * e4 + 4 * h]);
-        const f32x4 delta =
-            *reinterpret_cast<const f32x4*>(&s_row[i & 1][1][32 * r + 8 * e4 + 4 * h]);
+        const int first = 32 * half + 8 * e4 + 4 * h;
+        const f32x4 lse = *reinterpret_cast<const f32x4*>(&s_row[i % 3][0][first]);
+        const f32x4 delta = *reinterpret_cast<const f32x4*>(&s_row[i % 3][1][first]);
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const int e = 4 * e4 + f;
           const int at = 8 * e4 + 4 * h + f, p = p0 + at;
-          float x = s[e] * d.scale2, slant = 1.f;
-          if (capped) {
-            const float th = tanh_cap(x);
-            x = d.cap2 * th;
-            slant = 1.f - th * th;
-          }
-          if (sloped) x -= slope2 * fabsf((float)(p - key));
-          float w = exp2_fast(x - lse[f] * kLog2e);
+          float slant = 1.f;
+          float w = exp2_fast(score<MORE>(s[e], d, capped, sloped, slope2, p - key, lse[f], slant));
           float ds = w * (dp[e] - delta[f]);
           if (capped) ds *= slant;
-          if (!all) {
-            const bool seen = at < n && key < t.lk && mask.sees(p, key);
+          if (masked) {
+            const bool seen = (p >= from) & (p < to);
             w = seen ? w : 0.f;
             ds = seen ? ds : 0.f;
           }
@@ -261,36 +354,115 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs d) {
           dp[e] = ds;
         }
       }
+    };
+    if (rows == 32 && keys == 32 && mask.all(p0, p0 + 31, j0, j1))
+      weigh(std::false_type{});
+    else
+      weigh(std::true_type{});
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bf16x8 w = operand_of(s, u), ds = operand_of(dp, u);
+    for (int u = 0; u < 2; ++u) {
+      const bf16x8 w = operand_of(s, u), ds = operand_of(dp, u);
 #pragma unroll
-        for (int c = 0; c < DT; ++c) {
-          if (PAD && 32 * c >= D) break;
-          dv[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(gt(32 * r + 16 * u, c), w, dv[c], 0, 0, 0);
-          dk[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qt(32 * r + 16 * u, c), ds, dk[c], 0, 0, 0);
-        }
+      for (int c = 0; c < DT; ++c) {
+        if (PAD && 32 * c >= D) break;
+        dv[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(gt(16 * u, c), w, dv[c], 0, 0, 0);
+        dk[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qt(16 * u, c), ds, dk[c], 0, 0, 0);
       }
     }
   }
-  if (keys <= 0) return;
-  const bool in = key < t.lk;
-  uint16_t* const ok = a.dk + (t.k0 + key) * a.ld_dk + (int64_t)kv * D;
-  uint16_t* const ov = a.dv + (t.k0 + key) * a.ld_dv + (int64_t)kv * D;
+
+  // the sums over the other half of the queries, 16 bytes a lane at a time
+  landed<0>();
+  static_assert(4 * 64 * 2 * 4 * DT * 16 <= sizeof(s_mem), "sums of four waves");
+  f32x4* const other = reinterpret_cast<f32x4*>(s_mem) + block * (64 * 8 * DT) + lane;
+  auto four = [](const f32x16 (&g)[DT], int c) {
+    const int e = 4 * (c & 3);
+    return f32x4{g[c >> 2][e], g[c >> 2][e + 1], g[c >> 2][e + 2], g[c >> 2][e + 3]};
+  };
+  if (half == 1) {
 #pragma unroll
-  for (int c = 0; c < DT; ++c) {
-    store_columns(dk[c], a.sm_scale, ok, 32 * c, h, D, in);
-    store_columns(dv[c], 1.f, ov, 32 * c, h, D, in);
+    for (int c = 0; c < 4 * DT; ++c) {
+      other[64 * c] = four(dk, c);
+      other[64 * (4 * DT + c)] = four(dv, c);
+    }
   }
+  __syncthreads();
+  if (half == 1 || keys <= 0) return;
+#pragma unroll
+  for (int c = 0; c < 4 * DT; ++c) {
+    const f32x4 x = other[64 * c], y = other[64 * (4 * DT + c)];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dk[c >> 2][4 * (c & 3) + e] += x[e], dv[c >> 2][4 * (c & 3) + e] += y[e];
+  }
+  if (d.parts > 1) {
+    f32x4* const to = part_of<DP>(d, (id / (a.kv_heads * d.parts)) * a.kv_heads + kv, part, block, lane);
+#pragma unroll
+    for (int c = 0; c < 4 * DT; ++c) {
+      to[64 * c] = four(dk, c);
+      to[64 * (4 * DT + c)] = four(dv, c);
+    }
+    return;
+  }
+  store_key_grads<DP>(a, t, dk, dv, kv, key, h, D);
 }
 
-hipError_t launch_attn_bwd(const fp8rl_attn_args& a, float* delta, hipStream_t stream) {
+// The parts of dk and dv of a workgroup's keys, added in order.
+template <int DP>
+__global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs d) {
+  constexpr int DT = DP / 32;
+  const fp8rl_attn_args& a = d.a;
+  const int lane = (int)(threadIdx.x & 63);
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int kv = (int)blockIdx.x % a.kv_heads;
+  const DocTile t = find_tile<kOwn, true>(a, (int)blockIdx.x / a.kv_heads, lane);
+  if (t.doc >= (int)a.docs || t.lk - t.first - 32 * wave <= 0) return;
+  f32x16 g[2][DT];
+#pragma unroll
+  for (int c = 0; c < DT; ++c) g[0][c] = zeros16(), g[1][c] = zeros16();
+  for (int part = 0; part < d.parts; ++part) {
+    const f32x4* const from = part_of<DP>(d, (int)blockIdx.x, part, wave, lane);
+#pragma unroll
+    for (int c = 0; c < 8 * DT; ++c) {
+      const f32x4 x = from[64 * c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[c / (4 * DT)][(c >> 2) % DT][4 * (c & 3) + e] += x[e];
+    }
+  }
+  store_key_grads<DP>(a, t, g[0], g[1], kv, t.first + 32 * wave + (lane & 31), lane >> 5, a.head_dim);
+}
+
+namespace {
+
+// Parts that a key tile's queries are dealt out in: enough workgroups for two to a CU. (What splitting
+// costs is the parts' way through memory, 8 bytes a value of dk and dv and part, each way.)
+int key_parts(int64_t Tk, int64_t docs, int kv_heads) {
+  const int64_t tiles = (Tk / kOwn + docs) * kv_heads;
+  return (int)max((int64_t)1, min((int64_t)kMostParts, 512 / max((int64_t)1, tiles)));
+}
+
+int padded(int head_dim) { return head_dim <= 64 ? 64 : 128; }
+
+}  // namespace
+
+size_t attn_bwd_workspace(int64_t Tq, int64_t Tk, int64_t docs, int q_heads, int kv_heads,
+                          int head_dim) {
+  const int64_t parts = key_parts(Tk, docs, kv_heads);
+  const int64_t stats = (2 * Tq * q_heads + 3) / 4 * 4;
+  const int64_t part = parts > 1 ? (Tk / kOwn + docs) * kv_heads * parts * kOwn * 2 : 0;
+  return (size_t)(stats + part * padded(head_dim)) * sizeof(float);
+}
+
+hipError_t launch_attn_bwd(const fp8rl_attn_args& a, float* workspace, hipStream_t stream) {
   AttnArgs q = attn_args(a, kOwn, a.Tq), k = attn_args(a, kOwn, a.Tk);
-  q.delta = k.delta = delta;
-  const dim3 grid_q((unsigned)(q.slots * a.q_heads)), grid_k((unsigned)(k.slots * a.kv_heads));
+  q.stats = k.stats = workspace;
+  k.parts = key_parts(a.Tk, a.docs, a.kv_heads);
+  k.part = workspace + (2 * a.Tq * a.q_heads + 3) / 4 * 4;
+  const dim3 block(64 * kWaves);
+  const dim3 grid_q((unsigned)(q.slots * a.q_heads)), grid_k((unsigned)(k.slots * a.kv_heads * k.parts)),
+      grid_j((unsigned)(k.slots * a.kv_heads));
   auto go = [&](auto dq, auto dkv) {
-    hipLaunchKernelGGL(dq, grid_q, dim3(64 * kWaves), 0, stream, q);
-    hipLaunchKernelGGL(dkv, grid_k, dim3(64 * kWaves), 0, stream, k);
+    hipLaunchKernelGGL(dq, grid_q, block, 0, stream, q);
+    hipLaunchKernelGGL(dkv, grid_k, dim3(512), 0, stream, k);
   };
   const bool more = a.cap > 0.f || a.slopes;
   if (a.head_dim == 64)
@@ -305,6 +477,12 @@ hipError_t launch_attn_bwd(const fp8rl_attn_args& a, float* delta, hipStream_t s
   else
     more ? go(attn_dq_kernel<128, false, true>, attn_dkv_kernel<128, false, true>)
          : go(attn_dq_kernel<128, false, false>, attn_dkv_kernel<128, false, false>);
+  if (k.parts > 1) {
+    if (padded(a.head_dim) == 64)
+      hipLaunchKernelGGL(attn_dkv_join_kernel<64>, grid_j, block, 0, stream, k);
+    else
+      hipLaunchKernelGGL(attn_dkv_join_kernel<128>, grid_j, block, 0, stream, k);
+  }
   return hipGetLastError();
 }
 

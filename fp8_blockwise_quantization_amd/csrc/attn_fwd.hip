@@ -58,13 +58,13 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
   const int tiles = in_prefix + max(0, (mask.hi(last) + kK - 1) / kK - begin);
   auto key_of = [&](int i) { return kK * (i < in_prefix ? i : i - in_prefix + begin); };
 
-  const RowLoader<DP, kK, kWaves> load_k(a.ld_k, D, wave, lane), load_v(a.ld_v, D, wave, lane);
+  const RowLoader<DP, kK, kWaves> rows_in(D, wave, lane);
   const uint16_t* const k0 = a.k + t.k0 * a.ld_k + (int64_t)kv * D;
   const uint16_t* const v0 = a.v + t.k0 * a.ld_v + (int64_t)kv * D;
   auto load = [&](int i) {
     const int j = key_of(i);
-    load_k.load(k0 + j * a.ld_k, t.lk - j, s_k[i & 1], wave);
-    load_v.load(v0 + j * a.ld_v, t.lk - j, s_v[i & 1], wave);
+    rows_in.load(k0 + j * a.ld_k, a.ld_k, t.lk - j, s_k[i & 1], wave);
+    rows_in.load(v0 + j * a.ld_v, a.ld_v, t.lk - j, s_v[i & 1], wave);
   };
 
   const bool capped = MORE && a.cap > 0.f, sloped = MORE && a.slopes;
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int j = j0 + 32 * r + 8 * (e >> 2) + 4 * h + (e & 3);
-          s[r][e] = j < mask.prefix || (j >= lo && j < hi) ? s[r][e] : -__builtin_inff();
+          s[r][e] = (j < mask.prefix) | ((j >= lo) & (j < hi)) ? s[r][e] : -__builtin_inff();
         }
     }
     float top = fmaxf(s[0][0], s[1][0]);

@@ -20,7 +20,9 @@ hipError_t launch_attn_decode(const fp8rl_attn_decode_args& a, void* workspace, 
 hipError_t launch_attn_fwd(const fp8rl_attn_args& a, hipStream_t stream);
 
 // ---- attn_bwd.hip
-hipError_t launch_attn_bwd(const fp8rl_attn_args& a, float* delta, hipStream_t stream);
+size_t attn_bwd_workspace(int64_t Tq, int64_t Tk, int64_t docs, int q_heads, int kv_heads,
+                          int head_dim);
+hipError_t launch_attn_bwd(const fp8rl_attn_args& a, float* workspace, hipStream_t stream);
 
 // ---- kv_read.hip
 hipError_t launch_kv_read(const fp8rl_kv_read_args& a, hipStream_t stream);

@@ -16,7 +16,9 @@ namespace fp8rl {
 // The plain arguments, and what the launch adds.
 struct AttnArgs {
   fp8rl_attn_args a;
-  float* delta;  // backward: [q_heads][Tq], <dout, out>
+  float* stats;  // backward: [2][q_heads][Tq], lse in units of ln 2 and <dout, out>
+  float* part;   // sums of dk and dv in parts
+  int parts;
   int group;     // query heads of a key head
   int slots;     // tiles of rows, every document's last one counted whole
   float scale2;  // sm_scale log2(e); capped: sm_scale / cap
@@ -29,6 +31,7 @@ inline AttnArgs attn_args(const fp8rl_attn_args& a, int tile, int64_t T) {
   d.a.window = min(a.window, 1 << 25);  // past every distance; positions less a window stay in range
   d.group = a.q_heads / a.kv_heads;
   d.slots = (int)(T / tile + a.docs);
+  d.parts = 1;
   d.scale2 = a.cap > 0.f ? a.sm_scale / a.cap : a.sm_scale * kLog2e;
   d.cap2 = a.cap * kLog2e;
   return d;
@@ -73,7 +76,7 @@ struct Mask {
   __device__ __forceinline__ int hi(int p) const { return causal ? min(p + 1, lk) : lk; }
   __device__ __forceinline__ int lo(int p) const { return window ? max(0, p - window + 1) : 0; }
   __device__ __forceinline__ bool sees(int p, int j) const {
-    return j < prefix || (j >= lo(p) && j < hi(p));
+    return (j < prefix) | ((j >= lo(p)) & (j < hi(p)));
   }
   // Whether queries at positions p0 <= .. <= p1 see all (any) of the keys j0 <= .. < j1.
   __device__ __forceinline__ bool all(int p0, int p1, int j0, int j1) const {
@@ -119,9 +122,10 @@ __device__ __forceinline__ void dma_floats(const void* base, uint32_t off, const
                :: "v"(off), "s"(scalar_ptr(base)), "{m0}"(m0) : "memory");
 }
 
-// This wave's loads have arrived and its reads of LDS are done, and so with the others.
+// This wave's loads but the last N have arrived and its reads of LDS are done, and so with the others.
+template <int N = 0>
 __device__ __forceinline__ void landed() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // N rows of a matrix (pitch ld) into LDS by W waves, those from `rows` on as copies of the last
@@ -133,21 +137,19 @@ struct RowLoader {
   static constexpr int kOps = N / kRows / W;     // of a wave
   static_assert(kOps * kRows * W == N, "rows of a tile");
   static_assert(kRows * W % (DP == 64 ? 8 : 16) == 0, "one swizzle for a lane's rows");
-  int row[kOps];
+  int row;          // of the first load; the others' are W * kRows further each
   uint32_t column;  // bytes
-  uint32_t pitch;   // bytes
 
-  __device__ __forceinline__ RowLoader(int64_t ld, int head_dim, int wave, int lane)
-      : pitch((uint32_t)ld * 2) {
-#pragma unroll
-    for (int i = 0; i < kOps; ++i) row[i] = (i * W + wave) * kRows + lane / kChunks;
-    const int c = (lane % kChunks) ^ swizzle<DP>(row[0]);
+  __device__ __forceinline__ RowLoader(int head_dim, int wave, int lane)
+      : row(wave * kRows + lane / kChunks) {
+    const int c = (lane % kChunks) ^ swizzle<DP>(row);
     column = 8 * c < head_dim ? 16 * c : 0;
   }
-  __device__ __forceinline__ void load(const uint16_t* first, int rows, uint8_t* lds, int wave) const {
+  __device__ __forceinline__ void load(const uint16_t* first, int64_t ld, int rows, uint8_t* lds,
+                                       int wave) const {
 #pragma unroll
     for (int i = 0; i < kOps; ++i)
-      dma_rows(first, (uint32_t)min(row[i], rows - 1) * pitch + column,
+      dma_rows(first, (uint32_t)min(row + i * W * kRows, rows - 1) * ((uint32_t)ld * 2) + column,
                lds + (i * W + wave) * 1024);
   }
 };

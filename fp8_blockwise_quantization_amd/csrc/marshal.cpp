@@ -537,7 +537,10 @@ int attn_bwd(PyObject* const* a) {
              rv = matrix(tensor(a[17], "dv", dev), "dv", kBf16, r.Tk, kc);
   r.dout = (uint16_t*)rg.p, r.ld_dout = rg.ld, r.dq = (uint16_t*)rq.p, r.ld_dq = rq.ld;
   r.dk = (uint16_t*)rk.p, r.ld_dk = rk.ld, r.dv = (uint16_t*)rv.p, r.ld_dv = rv.ld;
-  const Workspace ws(a[18], fp8rl_attn_bwd_workspace_bytes(r.Tq, r.q_heads), dout, dev);
+  const Workspace ws(a[18],
+                     fp8rl_attn_bwd_workspace_bytes(r.Tq, r.Tk, r.docs, r.q_heads, r.kv_heads,
+                                                    r.head_dim),
+                     dout, dev);
   void* stream = stream_of(a[20]);
   int status;
   Py_BEGIN_ALLOW_THREADS

@@ -175,7 +175,7 @@ fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream);
  * sees get zeros. P and dS are rounded to bf16 for their products; sums are float32; each result is
  * rounded once. Deterministic: no atomics. Values of q, k, v and dout that are NaN or infinite reach
  * any row of their document, and no other document. Requires what fp8rl_attn_fwd does.
- *   workspace : at least fp8rl_attn_bwd_workspace_bytes(Tq, q_heads) bytes, 16-byte aligned,
+ *   workspace : at least fp8rl_attn_bwd_workspace_bytes(...) bytes, 16-byte aligned,
  *               overwritten
  * dq, dk and dv must not overlap the inputs or each other (columns of one fused row are fine).
  */
@@ -183,7 +183,8 @@ fp8rl_status fp8rl_attn_bwd(const fp8rl_attn_args* args, void* workspace, size_t
                             void* stream);
 
 /* Bytes of workspace fp8rl_attn_bwd needs. Host-only. */
-size_t fp8rl_attn_bwd_workspace_bytes(int64_t Tq, int32_t q_heads);
+size_t fp8rl_attn_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_heads,
+                                      int32_t kv_heads, int32_t head_dim);
 
 #ifdef __cplusplus
 }

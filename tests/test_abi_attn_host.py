@@ -214,10 +214,12 @@ def test_fwd_refusals(L):
 
 
 def test_bwd_refusals(L):
-    need = L.fp8rl_attn_bwd_workspace_bytes(100, 4)
-    assert need == 100 * 4 * 4
-    for bad in ((-1, 4), (1 << 24, 4), (100, 0), (100, 4097)):
-        assert L.fp8rl_attn_bwd_workspace_bytes(*bad) == 0
+    need = L.fp8rl_attn_bwd_workspace_bytes(100, 120, 3, 4, 2, 128)
+    assert need >= 2 * 100 * 4 * 4
+    assert L.fp8rl_attn_bwd_workspace_bytes(1 << 20, 1 << 20, 1, 4, 2, 128) == 2 * (1 << 20) * 4 * 4
+    for bad in ((-1, 120, 3, 4, 2, 128), (1 << 24, 120, 3, 4, 2, 128), (100, 120, 3, 0, 2, 128),
+                (100, 120, 3, 4, 3, 128), (100, 120, 3, 4, 2, 136), (100, 120, -1, 4, 2, 128)):
+        assert L.fp8rl_attn_bwd_workspace_bytes(*bad) == 0, bad
 
     def call(ws=A, wsb=1 << 40, **k):
         return L.fp8rl_attn_bwd(ctypes.byref(_attn.AttnArgs(**dict(DOCS, **k))), ws, wsb, None)

@@ -315,7 +315,7 @@ def test_repeats():
     runs = [d.fwd() for _ in range(2)]
     assert torch.equal(runs[0][0][3:-2], runs[1][0][3:-2])
     g = []
-    need = fq.fp8rl_attn_bwd_workspace_bytes(d.Tq, d.Hq)
+    need = fq.fp8rl_attn_bwd_workspace_bytes(d.Tq, d.Tk, 2, d.Hq, d.Hkv, d.D)
     for fill in (0, 255):
         ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
         g.append(fq.attn_bwd(d.dout.cuda(), *d.dev, *runs[0], 128, d.q_offsets, workspace=ws, **d.args))
