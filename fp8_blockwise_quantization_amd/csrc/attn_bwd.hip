@@ -48,42 +48,11 @@ struct QueryTiles {
   }
 };
 
-// The exponent of a weight, in units of ln 2: the score of a product s at distance p - j, less lse. With
-// a cap, the slope of the capped score there.
-template <bool MORE>
-__device__ __forceinline__ float score(float s, const AttnArgs& d, bool capped, bool sloped,
-                                       float slope2, int distance, float lse2, float& slant) {
-  if (!MORE) return __builtin_fmaf(s, d.scale2, -lse2);
-  float x = s * d.scale2;
-  if (capped) {
-    const float th = tanh_cap(x);
-    x = d.cap2 * th;
-    slant = 1.f - th * th;
-  }
-  if (sloped) x -= slope2 * fabsf((float)distance);
-  return x - lse2;
-}
-
 // Where a wave's lane keeps its part of dk (and behind it dv) of the keys of workgroup `tile`.
 template <int DP>
 __device__ __forceinline__ f32x4* part_of(const AttnArgs& d, int tile, int part, int wave, int lane) {
   return reinterpret_cast<f32x4*>(d.part) +
          (((int64_t)tile * d.parts + part) * kWaves + wave) * (2 * 32 * DP / 4) + lane;
-}
-
-template <int DP>
-__device__ __forceinline__ void store_key_grads(const fp8rl_attn_args& a, const DocTile& t,
-                                                const f32x16 (&dk)[DP / 32],
-                                                const f32x16 (&dv)[DP / 32], int kv, int key, int h,
-                                                int D) {
-  const bool in = key < t.lk;
-  uint16_t* const ok = a.dk + (t.k0 + key) * a.ld_dk + (int64_t)kv * D;
-  uint16_t* const ov = a.dv + (t.k0 + key) * a.ld_dv + (int64_t)kv * D;
-#pragma unroll
-  for (int c = 0; c < DP / 32; ++c) {
-    store_columns(dk[c], a.sm_scale, ok, 32 * c, h, D, in);
-    store_columns(dv[c], 1.f, ov, 32 * c, h, D, in);
-  }
 }
 
 }  // namespace
@@ -176,15 +145,21 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
     const ColOperand<DP> kt(s_k[i & 1], lane);
     f32x16 s, dp;
     auto weigh = [&](int r, auto masked) {  // dS in its place
+      if (MORE) {
+        const float from = (float)(p - j0 - 32 * r - 4 * h);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dp[e] -= delta;
+        finish_scores(
+            s, d, capped, sloped, slope2,
+            [&](int e) { return from - (float)(8 * (e >> 2) + (e & 3)); },
+            [&](int e, float th) { dp[e] *= 1.f - th * th; });
+      }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int j = j0 + 32 * r + 8 * (e >> 2) + 4 * h + (e & 3);
-        float slant = 1.f;
-        const float x = score<MORE>(s[e], d, capped, sloped, slope2, p - j, lse2, slant);
-        float ds = exp2_fast(x) * (dp[e] - delta);
-        if (capped) ds *= slant;
-        if (masked) ds = (j < mask.prefix) | ((j >= lo) & (j < hi)) ? ds : 0.f;
-        s[e] = ds;
+        const float x = MORE ? s[e] - lse2 : __builtin_fmaf(s[e], d.scale2, -lse2);
+        const float ds = exp2_fast(x) * (MORE ? dp[e] : dp[e] - delta);
+        s[e] = !masked || (j < mask.prefix) | ((j >= lo) & (j < hi)) ? ds : 0.f;
       }
     };
     const bool all = keys == kPass && mask.all(p0, p1, j0, j0 + kPass);
@@ -332,27 +307,26 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnArgs d) {
         from = key >= t.lk ? INT_MAX : prefixed || !mask.causal ? INT_MIN : key;
         to = min(p0 + rows, prefixed || !mask.window ? INT_MAX : key + mask.window);
       }
+      const float* const lse = &s_row[i % 3][0][32 * half + 4 * h];
+      const float* const delta = &s_row[i % 3][1][32 * half + 4 * h];
+      auto at = [](int e) { return 8 * (e >> 2) + (e & 3); };  // the query of place e, from 4h on
+      if (MORE) {
 #pragma unroll
-      for (int e4 = 0; e4 < 4; ++e4) {
-        const int first = 32 * half + 8 * e4 + 4 * h;
-        const f32x4 lse = *reinterpret_cast<const f32x4*>(&s_row[i % 3][0][first]);
-        const f32x4 delta = *reinterpret_cast<const f32x4*>(&s_row[i % 3][1][first]);
+        for (int e = 0; e < 16; ++e) dp[e] -= delta[at(e)];
+        const float first = (float)(p0 + 4 * h - key);
+        finish_scores(
+            s, d, capped, sloped, slope2, [&](int e) { return first + (float)at(e); },
+            [&](int e, float th) { dp[e] *= 1.f - th * th; });
+      }
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int e = 4 * e4 + f;
-          const int at = 8 * e4 + 4 * h + f, p = p0 + at;
-          float slant = 1.f;
-          float w = exp2_fast(score<MORE>(s[e], d, capped, sloped, slope2, p - key, lse[f], slant));
-          float ds = w * (dp[e] - delta[f]);
-          if (capped) ds *= slant;
-          if (masked) {
-            const bool seen = (p >= from) & (p < to);
-            w = seen ? w : 0.f;
-            ds = seen ? ds : 0.f;
-          }
-          s[e] = w;
-          dp[e] = ds;
-        }
+      for (int e = 0; e < 16; ++e) {
+        const float x = MORE ? s[e] - lse[at(e)] : __builtin_fmaf(s[e], d.scale2, -lse[at(e)]);
+        const int p = p0 + 4 * h + at(e);
+        const bool seen = !masked || (p >= from) & (p < to);
+        const float w = seen ? exp2_fast(x) : 0.f;
+        const float ds = w * (MORE ? dp[e] : dp[e] - delta[at(e)]);
+        s[e] = w;
+        dp[e] = seen ? ds : 0.f;
       }
     };
     if (rows == 32 && keys == 32 && mask.all(p0, p0 + 31, j0, j1))
@@ -403,32 +377,47 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnArgs d) {
     }
     return;
   }
-  store_key_grads<DP>(a, t, dk, dv, kv, key, h, D);
+  const bool in = key < t.lk;
+  uint16_t* const ok = a.dk + (t.k0 + key) * a.ld_dk + (int64_t)kv * D;
+  uint16_t* const ov = a.dv + (t.k0 + key) * a.ld_dv + (int64_t)kv * D;
+#pragma unroll
+  for (int c = 0; c < DT; ++c) {
+    store_columns(dk[c], a.sm_scale, ok, 32 * c, h, D, in);
+    store_columns(dv[c], 1.f, ov, 32 * c, h, D, in);
+  }
 }
 
-// The parts of dk and dv of a workgroup's keys, added in order.
+// The parts of dk and dv of a workgroup's keys, added in order: a wave per 32 keys and 32 columns of
+// either.
 template <int DP>
 __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs d) {
   constexpr int DT = DP / 32;
   const fp8rl_attn_args& a = d.a;
   const int lane = (int)(threadIdx.x & 63);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int kv = (int)blockIdx.x % a.kv_heads;
-  const DocTile t = find_tile<kOwn, true>(a, (int)blockIdx.x / a.kv_heads, lane);
-  if (t.doc >= (int)a.docs || t.lk - t.first - 32 * wave <= 0) return;
-  f32x16 g[2][DT];
+  const int kv = (int)blockIdx.x % a.kv_heads, c = (int)blockIdx.y;
+  f32x4 x[kMostParts][4];
 #pragma unroll
-  for (int c = 0; c < DT; ++c) g[0][c] = zeros16(), g[1][c] = zeros16();
-  for (int part = 0; part < d.parts; ++part) {
-    const f32x4* const from = part_of<DP>(d, (int)blockIdx.x, part, wave, lane);
+  for (int part = 0; part < kMostParts; ++part) {
+    if (part >= d.parts) break;
+    const f32x4* const from = part_of<DP>(d, (int)blockIdx.x, part, wave, lane) + 64 * 4 * c;
 #pragma unroll
-    for (int c = 0; c < 8 * DT; ++c) {
-      const f32x4 x = from[64 * c];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) g[c / (4 * DT)][(c >> 2) % DT][4 * (c & 3) + e] += x[e];
-    }
+    for (int e = 0; e < 4; ++e) x[part][e] = from[64 * e];
   }
-  store_key_grads<DP>(a, t, g[0], g[1], kv, t.first + 32 * wave + (lane & 31), lane >> 5, a.head_dim);
+  const DocTile t = find_tile<kOwn, true>(a, (int)blockIdx.x / a.kv_heads, lane);
+  const int key = t.first + 32 * wave;
+  if (t.doc >= (int)a.docs || key >= t.lk) return;
+  f32x16 g = zeros16();
+#pragma unroll
+  for (int part = 0; part < kMostParts; ++part) {
+    if (part >= d.parts) break;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) g[e] += x[part][e >> 2][e & 3];
+  }
+  const int64_t row = t.k0 + key + (lane & 31);
+  uint16_t* const to = c < DT ? a.dk + row * a.ld_dk : a.dv + row * a.ld_dv;
+  store_columns(g, c < DT ? a.sm_scale : 1.f, to + (int64_t)kv * a.head_dim, 32 * (c % DT), lane >> 5,
+                a.head_dim, key + (lane & 31) < t.lk);
 }
 
 namespace {
@@ -459,7 +448,7 @@ hipError_t launch_attn_bwd(const fp8rl_attn_args& a, float* workspace, hipStream
   k.part = workspace + (2 * a.Tq * a.q_heads + 3) / 4 * 4;
   const dim3 block(64 * kWaves);
   const dim3 grid_q((unsigned)(q.slots * a.q_heads)), grid_k((unsigned)(k.slots * a.kv_heads * k.parts)),
-      grid_j((unsigned)(k.slots * a.kv_heads));
+      grid_j((unsigned)(k.slots * a.kv_heads), (unsigned)(2 * padded(a.head_dim) / 32));
   auto go = [&](auto dq, auto dkv) {
     hipLaunchKernelGGL(dq, grid_q, block, 0, stream, q);
     hipLaunchKernelGGL(dkv, grid_k, dim3(512), 0, stream, k);

@@ -98,15 +98,12 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
     }
     if (MORE) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float x = s[r][e] * d.scale2;
-          if (capped) x = d.cap2 * tanh_cap(x);
-          const int j = j0 + 32 * r + 8 * (e >> 2) + 4 * h + (e & 3);
-          if (sloped) x -= slope2 * fabsf((float)(p - j));
-          s[r][e] = x;
-        }
+      for (int r = 0; r < 2; ++r) {
+        const float from = (float)(p - j0 - 32 * r - 4 * h);
+        finish_scores(
+            s[r], d, capped, sloped, slope2,
+            [&](int e) { return from - (float)(8 * (e >> 2) + (e & 3)); }, [](int, float) {});
+      }
     }
     if (keys < kK || !mask.all(p0, p1, j0, j0 + kK)) {
       const int lo = mask.lo(p), hi = mask.hi(p);

@@ -87,6 +87,29 @@ struct Mask {
   }
 };
 
+// Scores of 16 products, in units of ln 2, in their places: capped, less slope2 times the distances
+// far(e). Where a cap is, `slope_at(e, th)` is told each tanh. The branches are the same for the whole
+// call, and outside the loops, so that these stay in one piece.
+template <typename Far, typename Slope>
+__device__ __forceinline__ void finish_scores(f32x16& s, const AttnArgs& d, bool capped, bool sloped,
+                                              float slope2, Far far, Slope slope_at) {
+  if (capped) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float th = tanh_cap(s[e] * d.scale2);
+      slope_at(e, th);
+      s[e] = d.cap2 * th;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] *= d.scale2;
+  }
+  if (sloped) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(-slope2, fabsf(far(e)), s[e]);
+  }
+}
+
 // ------------------------------------------------------------------------------ rows in LDS
 
 // A tile of rows of DP bf16 values, 16-byte chunks c of row r at place c ^ swizzle(r): reads of one
