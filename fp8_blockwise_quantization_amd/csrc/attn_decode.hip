@@ -4,7 +4,7 @@
 // a tile of keys updates the three; parts of a sequence meet as
 //   M = max m_i,  l = sum l_i 2^(m_i - M),  o = sum o_i 2^(m_i - M)      (scores in units of ln 2).
 //
-// A wave takes 32 keys at a time, for up to 16 query heads that share them:
+// A wave, one of eight, takes 32 keys at a time, for up to 16 query heads that share them:
 //   S^T = K Q^T   matrix instruction 16x16x32, rows = keys, columns = heads, twice;
 //   O^T += V^T P^T  the same, rows = columns of v, contracted over the 32 keys.
 // Row r of the first (second) product is key 8 (r / 4) + r % 4 (+ 4), so that the four rows a lane
@@ -22,18 +22,27 @@ namespace fp8rl {
 
 namespace {
 
-constexpr int kUnit = 128;    // keys of a workgroup's step: four waves of 32
-constexpr int kLeast = 4;     // units that are not split further
-constexpr int kGroups = 1024; // workgroups a large call is split into, a sequence's rest not counted
+constexpr int kWaves = 8;   // of a workgroup, and what a CU runs at once
+constexpr int kUnit = 32;   // keys of a wave's step
+constexpr int kWhole = 512; // keys up to which a sequence is not split
+constexpr int kLeast = 2;   // units of a piece
 
+// Who does what.
+//   Where no sequence has more than kWhole keys, a workgroup takes a sequence and head tile, its waves
+//   the sequence's units in turn; their parts meet in LDS, and that is all.
+//   Else a wave takes a head tile and a piece of all sequences' units in a row. As many waves as run
+//   at once all take the same number of units, however the lengths differ; a wave may so end one
+//   sequence, take others whole and begin a last one. What it has of a sequence that was cut goes to
+//   memory, and a second kernel joins it. The waves of a workgroup have neighbouring heads of the same
+//   keys, which a cache laid out by tokens has side by side.
 struct DecodeArgs {
   fp8rl_attn_decode_args a;
-  float* part;  // [slot][heads of a tile][head_dim], behind them [slot][heads of a tile][m, l]
+  float* part;  // [wave][ended, begun][heads of a tile][head_dim], behind them their [m, l]
   PageOf page_of;
   int group;   // query heads of a key head
   int tiles;   // of 16 query heads of a key head
-  int heads;   // kv_heads * tiles: workgroups that share a piece of a sequence
-  int slots;   // workgroups
+  int heads;   // kv_heads * tiles
+  int lots;    // pieces that all units are cut into; 0: a sequence each
 };
 
 struct Keys {
@@ -51,69 +60,60 @@ __device__ __forceinline__ Keys keys_of(const DecodeArgs& d, int b) {
   return k;
 }
 
-// The piece of a sequence that workgroups x * heads .. take: sequences in order, each in as many
-// pieces as its units fill at `per` units, at least one.
-struct Piece {
-  int b;       // B: none
-  int piece, pieces;
-  int before;  // pieces of the sequences before
-  Keys keys;
+// Sums over the lanes up to each.
+__device__ __forceinline__ int sum_upto(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
+// A sequence's place among all sequences' units, and what a wave takes of these.
+struct Place {
+  int b, before;  // sequence and the units in front of it
+  int per;
 };
 
-__device__ __forceinline__ int units_of_a_piece(const DecodeArgs& d, int lane) {
-  int64_t total = 0;
-  for (int c = 0; c < (int)d.a.B; c += 64) total += keys_of(d, c + lane).units;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
-  const int64_t per = (total * d.heads + kGroups - 1) / kGroups;
-  return __builtin_amdgcn_readfirstlane((int)max((int64_t)kLeast, per));
-}
-
-// Of piece x (by_piece) or of sequence x.
-__device__ __forceinline__ Piece find_piece(const DecodeArgs& d, int x, bool by_piece, int lane) {
-  const int per = units_of_a_piece(d, lane);
+// Of the sequence that holds unit per * lot (b = B: none does), or of sequence `b`.
+__device__ __forceinline__ Place find_place(const DecodeArgs& d, int lot, int b, int lane) {
+  const int B = (int)d.a.B;
+  const int front = sum_upto(keys_of(d, lane).units);  // most calls' only sequences
+  int total = __builtin_amdgcn_readlane(front, 63);
+  for (int c = 64; c < B; c += 64)
+    total += __builtin_amdgcn_readlane(sum_upto(keys_of(d, c + lane).units), 63);
+  const int per = max(kLeast, (int)((uint32_t)(total + d.lots - 1) / (uint32_t)d.lots));
   int base = 0;
-  for (int c = 0; c < (int)d.a.B; c += 64) {
-    const Keys k = keys_of(d, c + lane);
-    const int pieces = c + lane < d.a.B ? max(1, (k.units + per - 1) / per) : 0;
-    int upto = pieces;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(upto, o, 64);
-      if (lane >= o) upto += t;
+  for (int c = 0; c < B; c += 64) {
+    const int upto = base + (c == 0 ? front : sum_upto(keys_of(d, c + lane).units));
+    const uint64_t here = __ballot(c + lane < B && (lot >= 0 ? upto > lot * per : c + lane == b));
+    if (here) {
+      const int at = __builtin_ctzll(here);
+      return {c + at, at ? __builtin_amdgcn_readlane(upto, at - 1) : base, per};
     }
-    const uint64_t past = __ballot(by_piece ? base + upto > x : c + lane == x);
-    if (past) {
-      const int at = __builtin_ctzll(past);
-      Piece p;
-      p.b = c + at;
-      p.pieces = __builtin_amdgcn_readlane(pieces, at);
-      p.before = base + __builtin_amdgcn_readlane(upto, at) - p.pieces;
-      p.piece = x - p.before;
-      p.keys.first = __builtin_amdgcn_readlane(k.first, at);
-      p.keys.last = __builtin_amdgcn_readlane(k.last, at);
-      p.keys.unit = __builtin_amdgcn_readlane(k.unit, at);
-      p.keys.units = __builtin_amdgcn_readlane(k.units, at);
-      return p;
-    }
-    base += __builtin_amdgcn_readlane(upto, 63);
+    base = __builtin_amdgcn_readlane(upto, 63);
   }
-  return Piece{(int)d.a.B, 0, 0, 0, {0, 0, 0, 0}};
+  return {B, base, per};
 }
 
-// N 32-bit words at p, which is aligned to 8 bytes (4 for one word).
-template <int N>
+// N 32-bit words at p, which is aligned to 8 bytes (4 for one word). ONCE: not kept in the caches (for
+// v, whose lines an instruction takes whole: 57.8 -> 53.8 us at 64 x 4096; k's come half a line at a time,
+// and some were read twice).
+template <bool ONCE, int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
   typedef u32x4 __attribute__((aligned(8))) u32x4_8;
+  auto get = [](auto* at) { return ONCE ? __builtin_nontemporal_load(at) : *at; };
   if constexpr (N == 1) {
-    w[0] = *static_cast<const uint32_t*>(p);
+    w[0] = get(static_cast<const uint32_t*>(p));
   } else if constexpr (N == 2) {
-    const u32x2 t = *static_cast<const u32x2*>(p);
+    const u32x2 t = get(static_cast<const u32x2*>(p));
     w[0] = t.x, w[1] = t.y;
   } else {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const u32x4 t = static_cast<const u32x4_8*>(p)[i];
+      const u32x4 t = get(static_cast<const u32x4_8*>(p) + i);
       w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
     }
   }
@@ -126,85 +126,62 @@ __device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, bool high) {
 
 }  // namespace
 
-// DP: head_dim rounded up to 64, 128 or 256. CODES: an E4M3 cache.
-template <int DP, bool CODES>
-__global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs d) {
+// DP: head_dim rounded up to 64, 128 or 256. CODES: an E4M3 cache. SPLIT: pieces to waves.
+template <int DP, bool CODES, bool SPLIT>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs d) {
   constexpr int VW = DP / 16;                   // columns of v a lane holds
   constexpr int VN = CODES ? DP / 64 : DP / 32; // words of them
+  constexpr int VP = VN > 4 ? 2 : 1;            // parts in which they come, for want of registers
   constexpr int KN = CODES ? DP / 64 : DP / 32; // 16-byte loads of a key's row
   constexpr int EL = CODES ? 1 : 2;             // bytes of an element
   constexpr int OS = DP + 4;
-  __shared__ int64_t s_at[4][2][32];
-  __shared__ float s_o[4][16][OS];
-  __shared__ float s_m[4][16], s_l[4][16];
+  constexpr int kStep = SPLIT ? kUnit : kUnit * kWaves;
+  __shared__ int64_t s_at[kWaves][2][32];
+  __shared__ float s_o[SPLIT ? 1 : kWaves][SPLIT ? 1 : 16][SPLIT ? 1 : OS];
+  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   const fp8rl_attn_decode_args& a = d.a;
   const int lane = (int)(threadIdx.x & 63);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int g = lane >> 4, col = lane & 15;
   const int D = a.head_dim;
 
-  const int head = (int)blockIdx.x % d.heads;
-  const Piece w = find_piece(d, (int)blockIdx.x / d.heads, true, lane);
-  if (w.b >= (int)a.B) return;
-  const int kv = head / d.tiles, tile = head % d.tiles;
+  const int id = SPLIT ? (int)blockIdx.x * kWaves + wave : (int)blockIdx.x;
+  const int lot = id / d.heads, head = id - lot * d.heads;
+  if (SPLIT && lot >= d.lots) return;
+  const int kv = head / d.tiles, tile = head - kv * d.tiles;
   const int count = min(16, d.group - 16 * tile);  // query heads of this tile
   const int head0 = kv * d.group + 16 * tile;
-
-  // the piece's units, spread evenly over the sequence's pieces
-  const int u0 = w.keys.unit + (int)((int64_t)w.keys.units * w.piece / w.pieces);
-  const int u1 = w.keys.unit + (int)((int64_t)w.keys.units * (w.piece + 1) / w.pieces);
-  const int end = min(w.keys.last, u1 * kUnit);
-
-  // q, a head a column, its columns of the head in the order in which the keys' come
-  bf16x8 qf[DP / 32];
-  {
-    const int64_t row = (int64_t)w.b * a.ld_q + (int64_t)(head0 + col) * D;
-#pragma unroll
-    for (int i = 0; i < DP / 32; ++i) {
-      const int at = CODES ? 64 * (i / 2) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g;
-      u32x4 t{0u, 0u, 0u, 0u};
-      if (col < count && at < D) {
-        if (a.q_scale) {
-          uint32_t c[2];
-          load_words(c, static_cast<const uint8_t*>(a.q) + row + at);
-          const u32x2 lo = codes_bf16(c[0]), hi = codes_bf16(c[1]);
-          t = u32x4{lo.x, lo.y, hi.x, hi.y};
-        } else {
-          t = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + row + at);
-        }
-      }
-      qf[i] = __builtin_bit_cast(bf16x8, t);
-    }
-  }
   const bool capped = a.cap > 0.f, sloped = a.slopes != nullptr;
   // a score in units of ln 2, or of the cap
   float unit = a.sm_scale * (a.q_scale ? *a.q_scale : 1.f) * (CODES ? *a.k_scale : 1.f);
   unit *= capped ? 1.f / a.cap : kLog2e;
+  const float v_scale = CODES ? *a.v_scale : 1.f;
   const float cap2 = a.cap * kLog2e;
   const float slope2 = sloped && col < count ? a.slopes[head0 + col] * kLog2e : 0.f;
 
   const char* const kbase = static_cast<const char*>(a.k_cache) + kv * a.head_stride * EL;
   const char* const vbase = static_cast<const char*>(a.v_cache) + kv * a.head_stride * EL;
-  const int32_t* const table = a.page_table + (int64_t)w.b * a.ld_table;
   const int krow = 8 * (col >> 2) + (col & 3);  // the key of this lane's row, less 4 in the second
   // columns past head_dim are read from column 0 and cleared in K (q has zeros there, but 0 * NaN)
-  int kcol[KN];
-  uint32_t kkeep[KN];
-#pragma unroll
-  for (int i = 0; i < KN; ++i) {
-    const int at = i * (CODES ? 64 : 32) + g * (CODES ? 16 : 8);
-    kcol[i] = at < D ? at * EL : 0;
-    kkeep[i] = at < D ? ~0u : 0u;
-  }
+  auto column = [&](int i) { return i * (CODES ? 64 : 32) + g * (CODES ? 16 : 8); };
   const bool ragged = D != DP;
   const int vcol = col * VW < D ? col * VW * EL : 0;
+
+  // the piece of a sequence at hand: keys in steps from `base` on to `end`
+  int b, taken, stop, before;  // units behind this piece and the wave's last, before sequence b
+  bool whole, begun;           // the piece is the whole sequence, its beginning
+  Keys keys;
+  int base, end;
+  const int32_t* table;
+  bf16x8 qf[DP / 32];  // q, a head a column, its columns of the head in the order of the keys'
 
   // the key that this lane resolves of the tile at `base`: its page's number, then its row
   auto entry = [&](int base) {
     const int key = base + (lane & 31);
-    return key >= w.keys.first && key < end ? table[d.page_of(key)] : -1;
+    return key >= keys.first && key < end ? table[d.page_of(key)] : -1;
   };
-  uint64_t seen = 0, seen_next = 0;  // bit i: key i of the tile is seen
+  uint64_t seen;  // bit i: key i of the tile is seen
+  int next_page;
   auto resolve = [&](int base, int page, int slot) {
     const bool ok = page >= 0 && page < a.num_pages;
     const int key = base + (lane & 31);
@@ -215,264 +192,357 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs d) {
     return __ballot(ok) & 0xFFFFFFFFull;
   };
 
-  uint32_t kf[2][KN][4], vf[8][VN];
+  uint32_t kf[2][KN][4], vf[VP][8][VN / VP];
   auto load_k = [&](int slot) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const char* row = kbase + s_at[wave][slot][krow + 4 * r];
 #pragma unroll
-      for (int i = 0; i < KN; ++i) load_words(kf[r][i], row + kcol[i]);
+      for (int i = 0; i < KN; ++i)
+        load_words<false>(kf[r][i], row + (column(i) < D ? column(i) * EL : 0));
     }
   };
 
-  f32x4 o[VW];
+  auto load_v = [&](int slot, int part) {
 #pragma unroll
-  for (int t = 0; t < VW; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -__builtin_inff(), l = 0.f;
+    for (int e = 0; e < 8; ++e)
+      load_words<true>(vf[part][e], vbase + s_at[wave][slot][8 * g + e] + vcol + part * (4 * VN / VP));
+  };
 
-  int base = u0 * kUnit + 32 * wave;
-  int slot = 0;
-  if (base < end) {
-    seen = resolve(base, entry(base), 0);
-    load_k(0);
-  }
-  int next_page = entry(base + kUnit);
-  for (; base < end; base += kUnit, slot ^= 1) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) load_words(vf[e], vbase + s_at[wave][slot][8 * g + e] + vcol);
-    seen_next = resolve(base + kUnit, next_page, slot ^ 1);
-    next_page = entry(base + 2 * kUnit);
-
-    f32x4 s[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      f32x4 acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < KN; ++i) {
-        uint32_t* f = kf[r][i];
-        if (ragged) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] &= kkeep[i];
-        }
-        if constexpr (CODES) {
-          const u32x2 c0 = codes_bf16(f[0]), c1 = codes_bf16(f[1]), c2 = codes_bf16(f[2]),
-                      c3 = codes_bf16(f[3]);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, (u32x4{c0.x, c0.y, c1.x, c1.y})), qf[2 * i], acc, 0, 0, 0);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, (u32x4{c2.x, c2.y, c3.x, c3.y})), qf[2 * i + 1], acc, 0, 0,
-              0);
-        } else {
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, (u32x4{f[0], f[1], f[2], f[3]})), qf[i], acc, 0, 0, 0);
-        }
-      }
-      s[r] = acc;
-    }
-    if (base + kUnit < end) load_k(slot ^ 1);
-
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3] * unit;
-    if (capped) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = cap2 * tanh_cap(x[e]);
-    }
-    if (sloped) {
-      const float far = (float)(w.keys.last - 1 - base - 8 * g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] -= slope2 * (far - (float)e);
-    }
-    if (seen != 0xFFFFFFFFull) {
-      const uint32_t mine = (uint32_t)(seen >> (8 * g));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool in = (mine >> e) & 1;
-        x[e] = in ? x[e] : -__builtin_inff();
-#pragma unroll
-        for (int i = 0; i < VN; ++i) vf[e][i] = in ? vf[e][i] : 0u;
-      }
-    }
-    float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                      fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    if (__any(top > m)) {
-      const float was = m;
-      m = fmaxf(m, max_rows(top));
-      const float f = m == -__builtin_inff() ? 1.f : exp2_fast(was - m);
-      l *= f;
-#pragma unroll
-      for (int t = 0; t < VW; ++t) o[t] *= f;
-    }
-    const float ref = m == -__builtin_inff() ? 0.f : m;
-    float p[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = exp2_fast(x[e] - ref);
-    l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-
-    if constexpr (CODES) {
-      f16x8 pf;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) pf[e] = (_Float16)p[e];
-#pragma unroll
-      for (int i = 0; i < VN; ++i) {  // four columns
-        u32x2 c[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = codes_f16(vf[e][i]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const bool high = t & 1;
-          const u32x4 f{halves(c[0][t >> 1], c[1][t >> 1], high),
-                        halves(c[2][t >> 1], c[3][t >> 1], high),
-                        halves(c[4][t >> 1], c[5][t >> 1], high),
-                        halves(c[6][t >> 1], c[7][t >> 1], high)};
-          o[4 * i + t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, f), pf,
-                                                                o[4 * i + t], 0, 0, 0);
-        }
-      }
+  auto next = [&]() {  // the next piece: false if there is none
+    if (!SPLIT) {
+      keys = keys_of(d, b);
+      end = keys.last, base = (keys.unit + wave) * kUnit;
     } else {
-      bf16x8 hi, lo;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        hi[e] = (__bf16)p[e];
-        lo[e] = (__bf16)(p[e] - (float)hi[e]);
-      }
-#pragma unroll
-      for (int t = 0; t < VW; ++t) {
-        const bool high = t & 1;
-        const u32x4 f{halves(vf[0][t >> 1], vf[1][t >> 1], high),
-                      halves(vf[2][t >> 1], vf[3][t >> 1], high),
-                      halves(vf[4][t >> 1], vf[5][t >> 1], high),
-                      halves(vf[6][t >> 1], vf[7][t >> 1], high)};
-        o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), hi, o[t], 0, 0,
-                                                       0);
-        o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), lo, o[t], 0, 0,
-                                                       0);
+      for (;; ++b) {
+        if (b >= (int)a.B || taken >= stop) return false;
+        keys = keys_of(d, b);
+        const int from = taken - before, to = min(keys.units, from + stop - taken);
+        before += keys.units;
+        if (to == 0) continue;  // (a sequence without keys is left to the join)
+        begun = from == 0, whole = begun && to == keys.units;
+        taken += to - from;
+        end = min(keys.last, (keys.unit + to) * kUnit);
+        base = (keys.unit + from) * kUnit;
+        break;
       }
     }
-    seen = seen_next;
-  }
+    table = a.page_table + (int64_t)b * a.ld_table;
+    return true;
+  };
+  auto start = [&]() {  // its first loads
+    const int64_t row = (int64_t)b * a.ld_q + (int64_t)(head0 + col) * D;
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i) {
+      const int at = CODES ? 64 * (i / 2) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g;
+      u32x4 t{0u, 0u, 0u, 0u};
+      if (col < count && at < D) {
+        if (a.q_scale) {
+          uint32_t c[2];
+          load_words<false>(c, static_cast<const uint8_t*>(a.q) + row + at);
+          const u32x2 lo = codes_bf16(c[0]), hi = codes_bf16(c[1]);
+          t = u32x4{lo.x, lo.y, hi.x, hi.y};
+        } else {
+          t = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + row + at);
+        }
+      }
+      qf[i] = __builtin_bit_cast(bf16x8, t);
+    }
+    seen = 0;
+    if (base < end) {
+      seen = resolve(base, entry(base), 0);
+      load_k(0);
+    }
+    next_page = entry(base + kStep);
+  };
 
-  // the four waves' parts meet
-  l = sum_rows(l);
-  if (g == 0) s_m[wave][col] = m, s_l[wave][col] = l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int t = 0; t < VW; ++t) s_o[wave][col][(4 * g + i) * VW + t] = o[t][i];
+  b = lot;
+  if (SPLIT) {
+    const Place p = find_place(d, lot, 0, lane);
+    b = p.b, before = p.before, taken = lot * p.per, stop = taken + p.per;
   }
-  __syncthreads();
-  const int chunks = D / 8;
-  for (int c = (int)threadIdx.x; c < count * chunks; c += 256) {
-    const int h = c / chunks, at = 8 * (c - h * chunks);
-    const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
-    float sum = 0.f, r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  bool more = next();
+  if (more) start();
+  while (more) {
+    f32x4 o[VW];
+#pragma unroll
+    for (int t = 0; t < VW; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -__builtin_inff(), l = 0.f;
+    for (int slot = 0; base < end; base += kStep, slot ^= 1) {
+      load_v(slot, 0);
+      const uint64_t seen_next = resolve(base + kStep, next_page, slot ^ 1);
+      next_page = entry(base + 2 * kStep);
+
+      if (ragged) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < KN; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kf[r][i][j] = column(i) < D ? kf[r][i][j] : 0u;
+      }
+      f32x4 s[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        f32x4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+          const uint32_t* f = kf[r][i];
+          if constexpr (CODES) {
+            const u32x2 c0 = codes_bf16(f[0]), c1 = codes_bf16(f[1]), c2 = codes_bf16(f[2]),
+                        c3 = codes_bf16(f[3]);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, (u32x4{c0.x, c0.y, c1.x, c1.y})), qf[2 * i], acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, (u32x4{c2.x, c2.y, c3.x, c3.y})), qf[2 * i + 1], acc, 0, 0,
+                0);
+          } else {
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, (u32x4{f[0], f[1], f[2], f[3]})), qf[i], acc, 0, 0, 0);
+          }
+        }
+        s[r] = acc;
+      }
+      if (VP > 1) load_v(slot, 1);
+      if (VP == 1 && base + kStep < end) load_k(slot ^ 1);
+
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3] * unit;
+      if (capped) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = cap2 * tanh_cap(x[e]);
+      }
+      if (sloped) {
+        const float far = (float)(keys.last - 1 - base - 8 * g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] -= slope2 * (far - (float)e);
+      }
+      if (seen != 0xFFFFFFFFull) {
+        const uint32_t mine = (uint32_t)(seen >> (8 * g));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool in = (mine >> e) & 1;
+          x[e] = in ? x[e] : -__builtin_inff();
+#pragma unroll
+          for (int i = 0; i < VN; ++i)
+            vf[i * VP / VN][e][i % (VN / VP)] = in ? vf[i * VP / VN][e][i % (VN / VP)] : 0u;
+        }
+      }
+      float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+      if (__any(top > m)) {
+        const float was = m;
+        m = fmaxf(m, max_rows(top));
+        const float f = m == -__builtin_inff() ? 1.f : exp2_fast(was - m);
+        l *= f;
+#pragma unroll
+        for (int t = 0; t < VW; ++t) o[t] *= f;
+      }
+      const float ref = m == -__builtin_inff() ? 0.f : m;
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = exp2_fast(x[e] - ref);
+      l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+
+      if constexpr (CODES) {
+        f16x8 pf;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pf[e] = (_Float16)p[e];
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {  // four columns
+          u32x2 c[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) c[e] = codes_f16(vf[0][e][i]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const bool high = t & 1;
+            const u32x4 f{halves(c[0][t >> 1], c[1][t >> 1], high),
+                          halves(c[2][t >> 1], c[3][t >> 1], high),
+                          halves(c[4][t >> 1], c[5][t >> 1], high),
+                          halves(c[6][t >> 1], c[7][t >> 1], high)};
+            o[4 * i + t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, f), pf,
+                                                                  o[4 * i + t], 0, 0, 0);
+          }
+        }
+      } else {
+        bf16x8 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          hi[e] = (__bf16)p[e];
+          lo[e] = (__bf16)(p[e] - (float)hi[e]);
+        }
+#pragma unroll
+        for (int t = 0; t < VW; ++t) {
+          if (VP > 1 && t == VW / 2 && base + kStep < end) load_k(slot ^ 1);
+          const bool high = t & 1;
+          const auto& v = vf[t * VP / VW];
+          const int w = (t >> 1) % (VN / VP);
+          const u32x4 f{halves(v[0][w], v[1][w], high), halves(v[2][w], v[3][w], high),
+                        halves(v[4][w], v[5][w], high), halves(v[6][w], v[7][w], high)};
+          o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), hi, o[t], 0, 0,
+                                                         0);
+          o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), lo, o[t], 0, 0,
+                                                         0);
+        }
+      }
+      seen = seen_next;
+    }
+    l = sum_rows(l);
+    const int most = min(16, d.group);
+    if (SPLIT) {
+      const int done = b;
+      const bool direct = whole;
+      const int64_t row = (2 * (int64_t)id + begun) * most + col;
+      ++b;
+      more = next();
+      if (more) start();  // its first loads are under way while this piece is written
+      if (col < count) {
+        const float f = l == 0.f ? 0.f : v_scale / l;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = (4 * g + i) * VW;
+          if (at >= D) continue;
+          if (direct) {
+            uint16_t* const out = a.out + (int64_t)done * a.ld_out + (int64_t)(head0 + col) * D + at;
+#pragma unroll
+            for (int t = 0; t < VW; t += 4)
+              *reinterpret_cast<u32x2*>(out + t) = u32x2{pack2_bf16(o[t][i] * f, o[t + 1][i] * f),
+                                                         pack2_bf16(o[t + 2][i] * f, o[t + 3][i] * f)};
+          } else {
+#pragma unroll
+            for (int t = 0; t < VW; t += 4)
+              *reinterpret_cast<f32x4*>(d.part + row * D + at + t) =
+                  f32x4{o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]};
+          }
+        }
+        if (!direct && g == 0)
+          *reinterpret_cast<float2*>(d.part + 2 * (int64_t)d.lots * d.heads * most * D + 2 * row) =
+              float2{m, l};
+      }
+      continue;
+    }
+    if (g == 0) s_m[wave][col] = m, s_l[wave][col] = l;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (s_l[i][h] == 0.f) continue;  // saw no key (a NaN is not left out)
-      const float f = exp2_fast(s_m[i][h] - top);
-      sum += s_l[i][h] * f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] += s_o[i][h][at + k] * f;
+      for (int t = 0; t < VW; ++t) s_o[SPLIT ? 0 : wave][SPLIT ? 0 : col][SPLIT ? 0 : (4 * g + i) * VW + t] = o[t][i];
     }
-    if (w.pieces == 1) {
-      const float f = sum == 0.f ? 0.f : (CODES ? *a.v_scale : 1.f) / sum;
+    __syncthreads();
+    const int pairs = D / 2;
+    for (int c = (int)threadIdx.x; c < count * pairs; c += 64 * kWaves) {
+      const int h = (int)((uint32_t)c / (uint32_t)pairs), at = 2 * (c - h * pairs);
+      float top = s_m[0][h];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] *= f;
-      *reinterpret_cast<u32x4*>(a.out + (int64_t)w.b * a.ld_out + (int64_t)(head0 + h) * D + at) =
-          round8(r);
-    } else {
-      const int most = min(16, d.group);
-      const int64_t row = (int64_t)blockIdx.x * most + h;
-      float* part = d.part + row * D + at;
-      reinterpret_cast<f32x4*>(part)[0] = f32x4{r[0], r[1], r[2], r[3]};
-      reinterpret_cast<f32x4*>(part)[1] = f32x4{r[4], r[5], r[6], r[7]};
-      if (at == 0) {
-        float* ml = d.part + (int64_t)d.slots * most * D + 2 * row;
-        ml[0] = top, ml[1] = sum;
+      for (int i = 1; i < kWaves; ++i) top = fmaxf(top, s_m[i][h]);
+      float sum = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        // (a wave that saw no key has zeros; one that saw a NaN is not left out)
+        const float li = s_l[i][h], f = li == 0.f ? 0.f : exp2_fast(s_m[i][h] - top);
+        const float2 v = *reinterpret_cast<const float2*>(
+            &s_o[SPLIT ? 0 : i][SPLIT ? 0 : h][SPLIT ? 0 : at]);
+        sum += li * f;
+        x += v.x * f;
+        y += v.y * f;
       }
+      const float f = sum == 0.f ? 0.f : v_scale / sum;
+      *reinterpret_cast<uint32_t*>(a.out + (int64_t)b * a.ld_out + (int64_t)(head0 + h) * D + at) =
+          pack2_bf16(x * f, y * f);
     }
+    more = false;
   }
 }
 
-// A wave per sequence and query head: the parts of those sequences that were split.
-__global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs d) {
+// The parts of a sequence that was cut, for one query head. W waves share the parts, and then their sums.
+template <int W>
+__global__ __launch_bounds__(W > 1 ? 64 * W : 256) void attn_decode_join_kernel(DecodeArgs d) {
+  constexpr int kItems = W > 1 ? 1 : 4;  // of a workgroup
+  __shared__ float s_sum[W];
+  __shared__ f32x4 s_o[W][64];
   const fp8rl_attn_decode_args& a = d.a;
   const int lane = (int)(threadIdx.x & 63);
-  const int x = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int x = (int)blockIdx.x * kItems + wave / W, part = wave % W;
   const int b = x / a.q_heads, hq = x - b * a.q_heads;
   if (b >= (int)a.B) return;
-  const Piece w = find_piece(d, b, false, lane);
-  if (w.pieces == 1) return;
+  const Place place = find_place(d, -1, b, lane);
+  const Keys keys = keys_of(d, b);
+  const bool has = 4 * lane < a.head_dim;
+  u32x2* const out =
+      reinterpret_cast<u32x2*>(a.out + (int64_t)b * a.ld_out + (int64_t)hq * a.head_dim);
+  if (keys.units == 0) {
+    if (has && part == 0) out[lane] = u32x2{0u, 0u};
+    return;
+  }
+  const int lot = place.before / place.per;
+  const int pieces = (place.before + keys.units - 1) / place.per - lot + 1;
+  if (pieces == 1) return;
   const int kv = hq / d.group, in = hq - kv * d.group;
   const int most = min(16, d.group);
-  // row of the parts that the first piece of this head has, and from one piece to the next
-  const int64_t row0 = ((int64_t)w.before * d.heads + kv * d.tiles + in / 16) * most + in % 16;
-  const int64_t step = (int64_t)d.heads * most;
-  const float* const ml = d.part + (int64_t)d.slots * most * a.head_dim;
+  // the row that piece i left: the first began the sequence, the others end it or go on
+  auto row_of = [&](int i) {
+    return (2 * ((int64_t)(lot + i) * d.heads + kv * d.tiles + in / 16) + (i == 0)) * most + in % 16;
+  };
+  const float* const ml = d.part + 2 * (int64_t)d.lots * d.heads * most * a.head_dim;
 
   float top = -__builtin_inff();
-  for (int c = lane; c < w.pieces; c += 64) top = fmaxf(top, ml[2 * (row0 + c * step)]);
+  for (int c = lane; c < pieces; c += 64) top = fmaxf(top, ml[2 * row_of(c)]);
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
 
-  const bool has = 4 * lane < a.head_dim;
   f32x4 o{0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
-  for (int c = 0; c < w.pieces; c += 64) {
+  for (int c = 16 * part; c < pieces; c += 16 * W) {  // sixteen in flight
+    f32x4 t[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      t[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (has && c + j < pieces)
+        t[j] = reinterpret_cast<const f32x4*>(d.part + row_of(c + j) * a.head_dim)[lane];
+    }
     float f = 0.f;
-    if (c + lane < w.pieces) {
-      const float* at = ml + 2 * (row0 + (c + lane) * step);
+    if (lane < 16 && c + lane < pieces) {
+      const float* at = ml + 2 * row_of(c + lane);
       f = at[1] == 0.f ? 0.f : exp2_fast(at[0] - top);
       sum += at[1] * f;
     }
-    const int n = min(64, w.pieces - c);
-    for (int i = 0; i < n; i += 8) {  // eight parts in flight
-      f32x4 t[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        t[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (has && i + j < n)
-          t[j] = reinterpret_cast<const f32x4*>(d.part +
-                                                (row0 + (c + i + j) * step) * a.head_dim)[lane];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        o += t[j] * __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), i + j));
-    }
+    for (int j = 0; j < 16; ++j)
+      o += t[j] * __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), j));
   }
   sum = wave_sum(sum);
-  const float f = sum == 0.f ? 0.f : (a.v_scale ? *a.v_scale : 1.f) / sum;
-  if (has) {
-    u32x2* out = reinterpret_cast<u32x2*>(a.out + (int64_t)b * a.ld_out + (int64_t)hq * a.head_dim);
-    out[lane] = u32x2{pack2_bf16(o[0] * f, o[1] * f), pack2_bf16(o[2] * f, o[3] * f)};
+  if (W > 1) {
+    if (lane == 0) s_sum[wave] = sum;
+    s_o[wave][lane] = o;
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) sum += s_sum[i], o += s_o[i][lane];
   }
+  const float f = sum == 0.f ? 0.f : (a.v_scale ? *a.v_scale : 1.f) / sum;
+  if (has) out[lane] = u32x2{pack2_bf16(o[0] * f, o[1] * f), pack2_bf16(o[2] * f, o[3] * f)};
 }
 
 namespace {
 
-// Workgroups for sequences of up to max_keys keys: kGroups and what each sequence's last piece adds,
-// or every piece that the smallest division gives, if that is less.
-struct Grid {
-  int64_t slots;
-  bool split;  // some sequence may be
-};
-Grid decode_grid(int64_t B, int64_t heads, int64_t max_keys, int window) {
-  int64_t units = (max_keys + kUnit - 1) / kUnit;
-  if (window) units = min(units, ((int64_t)window + kUnit - 2) / kUnit + 1);
-  const int64_t pieces = max((int64_t)1, (units + kLeast - 1) / kLeast);
-  const int64_t items = B * heads;
-  return {min(items * pieces, items + kGroups), pieces > 1};
+// Pieces of all sequences' units, 0 where a workgroup takes a sequence.
+int decode_lots(int64_t heads, int64_t max_keys, int window) {
+  if (window) max_keys = min(max_keys, (int64_t)window);
+  if (max_keys <= kWhole) return 0;
+  return (int)max((int64_t)1, 256 * kWaves / heads);
 }
 
-template <bool CODES>
+template <bool CODES, bool SPLIT>
 void run_decode(const DecodeArgs& d, hipStream_t stream) {
-  const dim3 grid((unsigned)d.slots), block(256);
+  const int64_t n = SPLIT ? ((int64_t)d.lots * d.heads + kWaves - 1) / kWaves : d.a.B * d.heads;
+  const dim3 grid((unsigned)n), block(64 * kWaves);
   if (d.a.head_dim <= 64)
-    hipLaunchKernelGGL((attn_decode_kernel<64, CODES>), grid, block, 0, stream, d);
+    hipLaunchKernelGGL((attn_decode_kernel<64, CODES, SPLIT>), grid, block, 0, stream, d);
   else if (d.a.head_dim <= 128)
-    hipLaunchKernelGGL((attn_decode_kernel<128, CODES>), grid, block, 0, stream, d);
+    hipLaunchKernelGGL((attn_decode_kernel<128, CODES, SPLIT>), grid, block, 0, stream, d);
   else
-    hipLaunchKernelGGL((attn_decode_kernel<256, CODES>), grid, block, 0, stream, d);
+    hipLaunchKernelGGL((attn_decode_kernel<256, CODES, SPLIT>), grid, block, 0, stream, d);
 }
 
 int head_tiles(int q_heads, int kv_heads) { return (q_heads / kv_heads + 15) / 16; }
@@ -481,10 +551,10 @@ int head_tiles(int q_heads, int kv_heads) { return (q_heads / kv_heads + 15) / 1
 
 size_t attn_decode_workspace(int64_t B, int q_heads, int kv_heads, int head_dim, int64_t max_keys,
                              int window) {
-  const Grid g = decode_grid(B, (int64_t)kv_heads * head_tiles(q_heads, kv_heads), max_keys, window);
-  if (!g.split) return 0;
-  return (size_t)g.slots * (size_t)min(16, q_heads / kv_heads) * (size_t)(head_dim + 2) *
-         sizeof(float);
+  if (B == 0) return 0;
+  const int64_t heads = (int64_t)kv_heads * head_tiles(q_heads, kv_heads);
+  return (size_t)(2 * heads * decode_lots(heads, max_keys, window)) *
+         (size_t)min(16, q_heads / kv_heads) * (size_t)(head_dim + 2) * sizeof(float);
 }
 
 hipError_t launch_attn_decode(const fp8rl_attn_decode_args& a, void* workspace, hipStream_t stream) {
@@ -495,15 +565,20 @@ hipError_t launch_attn_decode(const fp8rl_attn_decode_args& a, void* workspace, 
   d.group = a.q_heads / a.kv_heads;
   d.tiles = head_tiles(a.q_heads, a.kv_heads);
   d.heads = a.kv_heads * d.tiles;
-  const Grid g = decode_grid(a.B, d.heads, (int64_t)a.table_width * a.page_size, a.window);
-  d.slots = (int)g.slots;
-  if (a.k_scale)
-    run_decode<true>(d, stream);
+  d.lots = decode_lots(d.heads, (int64_t)a.table_width * a.page_size, a.window);
+  if (d.lots == 0) {
+    a.k_scale ? run_decode<true, false>(d, stream) : run_decode<false, false>(d, stream);
+    return hipGetLastError();
+  }
+  a.k_scale ? run_decode<true, true>(d, stream) : run_decode<false, true>(d, stream);
+  // a wave has sixteen of a sequence's parts in flight at a time; where there are more, eight waves share
+  // them
+  const int64_t items = a.B * a.q_heads;
+  if (d.lots <= 16 * a.B)
+    hipLaunchKernelGGL(attn_decode_join_kernel<1>, dim3((unsigned)((items + 3) / 4)), dim3(256), 0,
+                       stream, d);
   else
-    run_decode<false>(d, stream);
-  if (g.split)
-    hipLaunchKernelGGL(attn_decode_join_kernel, dim3((unsigned)((a.B * a.q_heads + 3) / 4)),
-                       dim3(256), 0, stream, d);
+    hipLaunchKernelGGL(attn_decode_join_kernel<8>, dim3((unsigned)items), dim3(512), 0, stream, d);
   return hipGetLastError();
 }
 

@@ -73,7 +73,7 @@ typedef struct {
  *               may be NULL when that is 0
  * Requires head_dim % 16 == 0, 16 <= head_dim <= 256, 1 <= kv_heads, q_heads a multiple of kv_heads,
  * q_heads <= 4096, B <= 65536, B * kv_heads * ceil(q_heads / kv_heads / 16) < 2^22, page_size >= 1,
- * table_width * page_size <= 2^30, num_pages * page_size < 2^62, sm_scale finite, window >= 0, cap
+ * table_width * page_size <= 2^30, B * table_width * page_size < 2^35, num_pages * page_size < 2^62, sm_scale finite, window >= 0, cap
  * finite and >= 0; bf16 pointers 16-byte and codes 8-byte aligned, pitches and strides multiples of 8
  * elements, ld_q, ld_out >= the columns, ld_table >= table_width, page_stride (with more than one
  * page), slot_stride and head_stride >= head_dim. B == 0 returns FP8RL_OK.

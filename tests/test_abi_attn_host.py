@@ -110,6 +110,7 @@ def test_decode_refusals(L):
         assert call(q_heads=h) == ESHAPE, h
     assert call(B=-1) == ESHAPE
     assert call(B=65537) == ESHAPE
+    assert call(B=65536, table_width=1 << 22, ld_table=1 << 22) == ESHAPE  # 2^42 keys in all
     assert call(B=65536, kv_heads=64, q_heads=64, ld_q=8192, ld_out=8192) == ESHAPE  # 2^22 pieces
     for v in (NAN, INF, -INF):
         assert call(sm_scale=v) == EARG, v
@@ -121,12 +122,12 @@ def test_decode_refusals(L):
 def test_decode_workspace(L):
     need = L.fp8rl_attn_decode_workspace_bytes
     assert need(4, 8, 2, 128, 512, 0) == 0  # nothing is split up to there
-    assert need(4, 8, 2, 128, 1 << 20, 300) == 0
-    assert need(4, 8, 2, 128, 513, 0) == 4 * 2 * 2 * 4 * 130 * 4
-    big = need(4, 8, 2, 128, 1 << 20, 0)
-    assert big > need(4, 8, 2, 128, 513, 0)
-    assert need(4, 8, 2, 128, 1 << 30, 0) == big  # bounded by the workgroups, not the length
+    assert need(4, 8, 2, 128, 1 << 20, 200) == 0
+    big = need(4, 8, 2, 128, 513, 0)
+    assert big == 2 * 2048 * 4 * 130 * 4  # two rows of four heads for each of 2048 waves
+    assert need(4, 8, 2, 128, 1 << 30, 0) == big  # bounded by the waves, not the length
     assert need(4, 8, 2, 128, 1 << 30, (1 << 31) - 1) == big
+    assert need(0, 8, 2, 128, 1 << 30, 0) == 0
     for bad in ((-1, 8, 2, 128, 513, 0), (4, 7, 2, 128, 513, 0), (4, 8, 2, 120, 513, 0),
                 (4, 8, 2, 128, -1, 0), (4, 8, 2, 128, (1 << 30) + 1, 0), (4, 8, 2, 128, 513, -1)):
         assert need(*bad) == 0, bad
