@@ -126,12 +126,12 @@ __device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, bool high) {
 
 }  // namespace
 
-// DP: head_dim rounded up to 64, 128 or 256. CODES: an E4M3 cache. SPLIT: pieces to waves.
-template <int DP, bool CODES, bool SPLIT>
+// DP: head_dim rounded up to 64, 128 or 256; PAD: it is less. CODES: an E4M3 cache. SPLIT: pieces to
+// waves.
+template <int DP, bool PAD, bool CODES, bool SPLIT>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs d) {
   constexpr int VW = DP / 16;                   // columns of v a lane holds
   constexpr int VN = CODES ? DP / 64 : DP / 32; // words of them
-  constexpr int VP = VN > 4 ? 2 : 1;            // parts in which they come, for want of registers
   constexpr int KN = CODES ? DP / 64 : DP / 32; // 16-byte loads of a key's row
   constexpr int EL = CODES ? 1 : 2;             // bytes of an element
   constexpr int OS = DP + 4;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
   const int lane = (int)(threadIdx.x & 63);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int g = lane >> 4, col = lane & 15;
-  const int D = a.head_dim;
+  const int D = PAD ? a.head_dim : DP;
 
   const int id = SPLIT ? (int)blockIdx.x * kWaves + wave : (int)blockIdx.x;
   const int lot = id / d.heads, head = id - lot * d.heads;
@@ -164,8 +164,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
   const int krow = 8 * (col >> 2) + (col & 3);  // the key of this lane's row, less 4 in the second
   // columns past head_dim are read from column 0 and cleared in K (q has zeros there, but 0 * NaN)
   auto column = [&](int i) { return i * (CODES ? 64 : 32) + g * (CODES ? 16 : 8); };
-  const bool ragged = D != DP;
-  const int vcol = col * VW < D ? col * VW * EL : 0;
+  const int vcol = !PAD || col * VW < D ? col * VW * EL : 0;
 
   // the piece of a sequence at hand: keys in steps from `base` on to `end`
   int b, taken, stop, before;  // units behind this piece and the wave's last, before sequence b
@@ -192,21 +191,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
     return __ballot(ok) & 0xFFFFFFFFull;
   };
 
-  uint32_t kf[2][KN][4], vf[VP][8][VN / VP];
+  uint32_t kf[2][KN][4], vf[8][VN];
   auto load_k = [&](int slot) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const char* row = kbase + s_at[wave][slot][krow + 4 * r];
 #pragma unroll
       for (int i = 0; i < KN; ++i)
-        load_words<false>(kf[r][i], row + (column(i) < D ? column(i) * EL : 0));
+        load_words<false>(kf[r][i], row + (!PAD || column(i) < D ? column(i) * EL : 0));
     }
-  };
-
-  auto load_v = [&](int slot, int part) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      load_words<true>(vf[part][e], vbase + s_at[wave][slot][8 * g + e] + vcol + part * (4 * VN / VP));
   };
 
   auto next = [&]() {  // the next piece: false if there is none
@@ -269,11 +262,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
     for (int t = 0; t < VW; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = -__builtin_inff(), l = 0.f;
     for (int slot = 0; base < end; base += kStep, slot ^= 1) {
-      load_v(slot, 0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        load_words<true>(vf[e], vbase + s_at[wave][slot][8 * g + e] + vcol);
       const uint64_t seen_next = resolve(base + kStep, next_page, slot ^ 1);
       next_page = entry(base + 2 * kStep);
 
-      if (ragged) {
+      if (PAD) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -303,8 +298,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
         }
         s[r] = acc;
       }
-      if (VP > 1) load_v(slot, 1);
-      if (VP == 1 && base + kStep < end) load_k(slot ^ 1);
+      if (base + kStep < end) load_k(slot ^ 1);
 
       float x[8];
 #pragma unroll
@@ -325,8 +319,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
           const bool in = (mine >> e) & 1;
           x[e] = in ? x[e] : -__builtin_inff();
 #pragma unroll
-          for (int i = 0; i < VN; ++i)
-            vf[i * VP / VN][e][i % (VN / VP)] = in ? vf[i * VP / VN][e][i % (VN / VP)] : 0u;
+          for (int i = 0; i < VN; ++i) vf[e][i] = in ? vf[e][i] : 0u;
         }
       }
       float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
@@ -353,7 +346,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
         for (int i = 0; i < VN; ++i) {  // four columns
           u32x2 c[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) c[e] = codes_f16(vf[0][e][i]);
+          for (int e = 0; e < 8; ++e) c[e] = codes_f16(vf[e][i]);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const bool high = t & 1;
@@ -374,12 +367,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
         }
 #pragma unroll
         for (int t = 0; t < VW; ++t) {
-          if (VP > 1 && t == VW / 2 && base + kStep < end) load_k(slot ^ 1);
           const bool high = t & 1;
-          const auto& v = vf[t * VP / VW];
-          const int w = (t >> 1) % (VN / VP);
-          const u32x4 f{halves(v[0][w], v[1][w], high), halves(v[2][w], v[3][w], high),
-                        halves(v[4][w], v[5][w], high), halves(v[6][w], v[7][w], high)};
+          const int w = t >> 1;
+          const u32x4 f{halves(vf[0][w], vf[1][w], high), halves(vf[2][w], vf[3][w], high),
+                        halves(vf[4][w], vf[5][w], high), halves(vf[6][w], vf[7][w], high)};
           o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), hi, o[t], 0, 0,
                                                          0);
           o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f), lo, o[t], 0, 0,
@@ -537,12 +528,17 @@ template <bool CODES, bool SPLIT>
 void run_decode(const DecodeArgs& d, hipStream_t stream) {
   const int64_t n = SPLIT ? ((int64_t)d.lots * d.heads + kWaves - 1) / kWaves : d.a.B * d.heads;
   const dim3 grid((unsigned)n), block(64 * kWaves);
-  if (d.a.head_dim <= 64)
-    hipLaunchKernelGGL((attn_decode_kernel<64, CODES, SPLIT>), grid, block, 0, stream, d);
-  else if (d.a.head_dim <= 128)
-    hipLaunchKernelGGL((attn_decode_kernel<128, CODES, SPLIT>), grid, block, 0, stream, d);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, d); };
+  const int D = d.a.head_dim;
+  if (D <= 64)
+    D == 64 ? go(attn_decode_kernel<64, false, CODES, SPLIT>)
+            : go(attn_decode_kernel<64, true, CODES, SPLIT>);
+  else if (D <= 128)
+    D == 128 ? go(attn_decode_kernel<128, false, CODES, SPLIT>)
+             : go(attn_decode_kernel<128, true, CODES, SPLIT>);
   else
-    hipLaunchKernelGGL((attn_decode_kernel<256, CODES, SPLIT>), grid, block, 0, stream, d);
+    D == 256 ? go(attn_decode_kernel<256, false, CODES, SPLIT>)
+             : go(attn_decode_kernel<256, true, CODES, SPLIT>);
 }
 
 int head_tiles(int q_heads, int kv_heads) { return (q_heads / kv_heads + 15) / 16; }

@@ -14,20 +14,25 @@ namespace fp8rl {
 
 namespace {
 
-constexpr int kQ = 128, kK = 64, kWaves = 4;
+constexpr int kQ = 128, kK = 64;
 constexpr float kRise = 8.f;
+constexpr int kFew = 512;  // workgroups up to which two waves share the keys
 
 }  // namespace
 
-// DP: head_dim rounded up to 64 or 128; PAD: it is less. MORE: capped scores or slopes.
-template <int DP, bool PAD, bool MORE>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
+// DP: head_dim rounded up to 64 or 128; PAD: it is less. MORE: capped scores or slopes. KH: waves that
+// share 32 queries, each with its part of a tile's keys; their sums meet in the end.
+template <int DP, bool PAD, bool MORE, int KH>
+__global__ __launch_bounds__(256 * KH, 2) void attn_fwd_kernel(AttnArgs d) {
   constexpr int KS = DP / 16, DT = DP / 32;
-  __shared__ __align__(1024) uint8_t s_k[2][kK * DP * 2];
-  __shared__ __align__(1024) uint8_t s_v[2][kK * DP * 2];
+  constexpr int kWaves = 4 * KH, NR = 2 / KH;  // a wave's 32-key parts of a tile
+  constexpr int kTile = kK * DP * 2;           // bytes
+  __shared__ __align__(1024) uint8_t s_mem[4 * kTile];  // k and v of two tiles; then O of some waves
+  __shared__ float s_m[4][32], s_l[4][32];
   const fp8rl_attn_args& a = d.a;
   const int lane = (int)(threadIdx.x & 63), h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int block = wave & 3, part = wave >> 2;  // of the queries, of a tile's keys
   const int D = PAD ? a.head_dim : DP;
 
   // key heads fastest (with 8 of them, one to an XCD and its L2), the last tiles of documents, which
@@ -39,10 +44,10 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
   if (t.doc >= (int)a.docs) return;
   const Mask mask(a, t);
   const int shift = t.lk - t.lq;
-  const int row = t.first + 32 * wave + (lane & 31);
+  const int row = t.first + 32 * block + (lane & 31);
   const int p = row + shift;
-  const int rows = min(32, t.lq - t.first - 32 * wave);  // of this wave
-  const int p0 = t.first + 32 * wave + shift, p1 = p0 + rows - 1;
+  const int rows = min(32, t.lq - t.first - 32 * block);  // of this wave
+  const int p0 = t.first + 32 * block + shift, p1 = p0 + rows - 1;
 
   bf16x8 q[KS];
   {
@@ -63,8 +68,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
   const uint16_t* const v0 = a.v + t.k0 * a.ld_v + (int64_t)kv * D;
   auto load = [&](int i) {
     const int j = key_of(i);
-    rows_in.load(k0 + j * a.ld_k, a.ld_k, t.lk - j, s_k[i & 1], wave);
-    rows_in.load(v0 + j * a.ld_v, a.ld_v, t.lk - j, s_v[i & 1], wave);
+    rows_in.load(k0 + j * a.ld_k, a.ld_k, t.lk - j, s_mem + 2 * (i & 1) * kTile, wave);
+    rows_in.load(v0 + j * a.ld_v, a.ld_v, t.lk - j, s_mem + (2 * (i & 1) + 1) * kTile, wave);
   };
 
   const bool capped = MORE && a.cap > 0.f, sloped = MORE && a.slopes;
@@ -80,44 +85,52 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
   for (int i = 0; i < tiles; ++i) {
     landed();
     if (i + 1 < tiles) load(i + 1);
-    const int j0 = key_of(i), keys = min(kK, t.lk - j0);
-    if (keys < kK) {
-      clear_rows<DP, kK, kWaves>(s_v[i & 1], keys);
+    uint8_t *const s_k = s_mem + 2 * (i & 1) * kTile, *const s_v = s_k + kTile;
+    const int tile = key_of(i), in_tile = min(kK, t.lk - tile);
+    if (in_tile < kK) {
+      clear_rows<DP, kK, kWaves>(s_v, in_tile);
       __syncthreads();
     }
-    if (rows <= 0 || !mask.any(p0, p1, j0, j0 + keys)) continue;
+    // this wave's keys
+    constexpr int kOwn = 32 * NR;
+    const int j0 = tile + kOwn * part, keys = min(kOwn, t.lk - j0);
+    if (rows <= 0 || keys <= 0 || !mask.any(p0, p1, j0, j0 + keys)) continue;
 
-    const RowOperand<DP> kop(s_k[i & 1], lane);
-    f32x16 s[2] = {zeros16(), zeros16()};
+    const RowOperand<DP> kop(s_k + kOwn * part * DP * 2, lane);
+    f32x16 s[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) s[r] = zeros16();
 #pragma unroll
     for (int c = 0; c < KS; ++c) {
       if (PAD && 16 * c >= D) break;
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < NR; ++r)
         s[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kop(32 * r, c), q[c], s[r], 0, 0, 0);
     }
     if (MORE) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < NR; ++r) {
         const float from = (float)(p - j0 - 32 * r - 4 * h);
         finish_scores(
             s[r], d, capped, sloped, slope2,
             [&](int e) { return from - (float)(8 * (e >> 2) + (e & 3)); }, [](int, float) {});
       }
     }
-    if (keys < kK || !mask.all(p0, p1, j0, j0 + kK)) {
+    if (keys < kOwn || !mask.all(p0, p1, j0, j0 + kOwn)) {
       const int lo = mask.lo(p), hi = mask.hi(p);
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int j = j0 + 32 * r + 8 * (e >> 2) + 4 * h + (e & 3);
           s[r][e] = (j < mask.prefix) | ((j >= lo) & (j < hi)) ? s[r][e] : -__builtin_inff();
         }
     }
-    float top = fmaxf(s[0][0], s[1][0]);
+    float top = s[0][0];
 #pragma unroll
-    for (int e = 1; e < 16; ++e) top = fmaxf(fmaxf(top, s[0][e]), s[1][e]);
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[r][e]);
     {
       const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top),
                                                       false, false);
@@ -134,7 +147,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
     const float ref = m == -__builtin_inff() ? 0.f : m;
     float sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         s[r][e] = exp2_fast(__builtin_fmaf(s[r][e], scale2, -ref));
@@ -142,9 +155,9 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
       }
     l += sum;
 
-    const ColOperand<DP> vop(s_v[i & 1], lane);
+    const ColOperand<DP> vop(s_v + kOwn * part * DP * 2, lane);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < 2 * NR; ++r) {
       const bf16x8 w = operand_of(s[r >> 1], r & 1);
 #pragma unroll
       for (int c = 0; c < DT; ++c) {
@@ -154,12 +167,40 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
     }
   }
 
-  if (rows <= 0) return;
   {
     const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false,
                                                     false);
     l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
   }
+  if (KH > 1) {
+    landed();
+    f32x4* const other = reinterpret_cast<f32x4*>(s_mem) + block * (64 * 4 * DT) + lane;
+    if (part == 1) {
+#pragma unroll
+      for (int c = 0; c < 4 * DT; ++c) {
+        const int e = 4 * (c & 3);
+        other[64 * c] = f32x4{o[c >> 2][e], o[c >> 2][e + 1], o[c >> 2][e + 2], o[c >> 2][e + 3]};
+      }
+      if (h == 0) s_m[block][lane] = m, s_l[block][lane] = l;
+    }
+    __syncthreads();
+    if (part == 1) return;
+    const float m1 = s_m[block][lane & 31], l1 = s_l[block][lane & 31], both = fmaxf(m, m1);
+    // (a wave that saw no key has zeros; one that saw a NaN is not left out)
+    const float f0 = l == 0.f ? 0.f : exp2_fast(m - both), f1 = l1 == 0.f ? 0.f : exp2_fast(m1 - both);
+    m = both;
+    l = l * f0 + l1 * f1;
+#pragma unroll
+    for (int c = 0; c < 4 * DT; ++c) {
+      const f32x4 x = other[64 * c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = 4 * (c & 3) + e;
+        o[c >> 2][at] = o[c >> 2][at] * f0 + x[e] * f1;
+      }
+    }
+  }
+  if (rows <= 0) return;
   const bool in = row < t.lq;
   const float f = l == 0.f ? 0.f : 1.f / l;
   uint16_t* const out = a.out + (t.q0 + row) * a.ld_out + (int64_t)head * D;
@@ -172,17 +213,27 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnArgs d) {
 
 hipError_t launch_attn_fwd(const fp8rl_attn_args& a, hipStream_t stream) {
   const AttnArgs d = attn_args(a, kQ, a.Tq);
-  const dim3 grid((unsigned)(d.slots * a.q_heads)), block(64 * kWaves);
+  const dim3 grid((unsigned)(d.slots * a.q_heads));
   const bool more = a.cap > 0.f || a.slopes;
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, d); };
+  const bool few = d.slots * a.q_heads <= kFew;
+  auto go = [&](auto one, auto two) {
+    if (few)
+      hipLaunchKernelGGL(two, grid, dim3(512), 0, stream, d);
+    else
+      hipLaunchKernelGGL(one, grid, dim3(256), 0, stream, d);
+  };
   if (a.head_dim == 64)
-    more ? go(attn_fwd_kernel<64, false, true>) : go(attn_fwd_kernel<64, false, false>);
+    more ? go(attn_fwd_kernel<64, false, true, 1>, attn_fwd_kernel<64, false, true, 2>)
+         : go(attn_fwd_kernel<64, false, false, 1>, attn_fwd_kernel<64, false, false, 2>);
   else if (a.head_dim < 64)
-    more ? go(attn_fwd_kernel<64, true, true>) : go(attn_fwd_kernel<64, true, false>);
+    more ? go(attn_fwd_kernel<64, true, true, 1>, attn_fwd_kernel<64, true, true, 2>)
+         : go(attn_fwd_kernel<64, true, false, 1>, attn_fwd_kernel<64, true, false, 2>);
   else if (a.head_dim < 128)
-    more ? go(attn_fwd_kernel<128, true, true>) : go(attn_fwd_kernel<128, true, false>);
+    more ? go(attn_fwd_kernel<128, true, true, 1>, attn_fwd_kernel<128, true, true, 2>)
+         : go(attn_fwd_kernel<128, true, false, 1>, attn_fwd_kernel<128, true, false, 2>);
   else
-    more ? go(attn_fwd_kernel<128, false, true>) : go(attn_fwd_kernel<128, false, false>);
+    more ? go(attn_fwd_kernel<128, false, true, 1>, attn_fwd_kernel<128, false, true, 2>)
+         : go(attn_fwd_kernel<128, false, false, 1>, attn_fwd_kernel<128, false, false, 2>);
   return hipGetLastError();
 }
 

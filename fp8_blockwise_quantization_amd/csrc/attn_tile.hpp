@@ -75,9 +75,6 @@ struct Mask {
         causal(a.causal) {}
   __device__ __forceinline__ int hi(int p) const { return causal ? min(p + 1, lk) : lk; }
   __device__ __forceinline__ int lo(int p) const { return window ? max(0, p - window + 1) : 0; }
-  __device__ __forceinline__ bool sees(int p, int j) const {
-    return (j < prefix) | ((j >= lo(p)) & (j < hi(p)));
-  }
   // Whether queries at positions p0 <= .. <= p1 see all (any) of the keys j0 <= .. < j1.
   __device__ __forceinline__ bool all(int p0, int p1, int j0, int j1) const {
     return j1 <= prefix || (j1 <= hi(p0) && j0 >= lo(p1));
