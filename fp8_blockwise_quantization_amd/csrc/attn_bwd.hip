@@ -48,6 +48,25 @@ struct QueryTiles {
   }
 };
 
+// Products s into scores in units of ln 2, in their places; with a cap, ds times the capped score's slope,
+// 1 - tanh^2 = -4 v (1 + v).
+template <typename Far>
+__device__ __forceinline__ void finish_scores(f32x16& s, f32x16& ds, const AttnArgs& d, bool capped,
+                                              bool sloped, float slope2, Far far) {
+  if (capped) {
+    cap_places(s, d);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      ds[e] *= -4.f * __builtin_fmaf(s[e], s[e], s[e]);
+      s[e] = __builtin_fmaf(s[e], 2.f * d.cap2, d.cap2);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] *= d.scale2;
+  }
+  if (sloped) slope_scores(s, 1.f, 0.f, slope2, far);
+}
+
 // Where a wave's lane keeps its part of dk (and behind it dv) of the keys of workgroup `tile`.
 template <int DP>
 __device__ __forceinline__ f32x4* part_of(const AttnArgs& d, int tile, int part, int wave, int lane) {
@@ -146,13 +165,11 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
     f32x16 s, dp;
     auto weigh = [&](int r, auto masked) {  // dS in its place
       if (MORE) {
-        const float from = (float)(p - j0 - 32 * r - 4 * h);
 #pragma unroll
         for (int e = 0; e < 16; ++e) dp[e] -= delta;
-        finish_scores(
-            s, d, capped, sloped, slope2,
-            [&](int e) { return from - (float)(8 * (e >> 2) + (e & 3)); },
-            [&](int e, float th) { dp[e] *= 1.f - th * th; });
+        const float from = (float)(p - j0 - 32 * r - 4 * h);
+        finish_scores(s, dp, d, capped, sloped, slope2,
+                      [&](int e) { return from - (float)(8 * (e >> 2) + (e & 3)); });
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -202,7 +219,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnArgs d) {
   __shared__ __align__(1024) float s_row[3][2][kQueries];  // lse and delta of the tile's queries
   // the steps of the keys' operand that do not fit the registers beside the sums (spilled, their
   // reloads would wait for the tiles in flight)
-  constexpr int kHeld = DP == 64 ? KS : MORE && PAD ? KS - 6 : KS - 4;
+  constexpr int kHeld = DP == 64 ? KS : MORE ? KS - 6 : KS - 4;
   __shared__ u32x4 s_k[4][KS - kHeld + 1][64];
   uint8_t* const s_v = s_mem + 6 * kTile;
   const fp8rl_attn_args& a = d.a;
@@ -314,9 +331,8 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnArgs d) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) dp[e] -= delta[at(e)];
         const float first = (float)(p0 + 4 * h - key);
-        finish_scores(
-            s, d, capped, sloped, slope2, [&](int e) { return first + (float)at(e); },
-            [&](int e, float th) { dp[e] *= 1.f - th * th; });
+        finish_scores(s, dp, d, capped, sloped, slope2,
+                      [&](int e) { return first + (float)at(e); });
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
