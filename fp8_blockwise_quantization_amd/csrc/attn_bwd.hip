@@ -100,6 +100,22 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
   const bool in = row < t.lq;
   const int64_t qrow = t.q0 + min(row, t.lq - 1);
 
+  const int first = t.first + shift, last = min(t.first + kOwn, t.lq) - 1 + shift;
+  const int in_prefix = (mask.prefix + kPass - 1) / kPass;
+  const int begin = max(mask.lo(first) / kPass, in_prefix);
+  const int tiles = in_prefix + max(0, (mask.hi(last) + kPass - 1) / kPass - begin);
+  auto key_of = [&](int i) { return kPass * (i < in_prefix ? i : i - in_prefix + begin); };
+
+  const RowLoader<DP, kPass, kWaves> rows_in(D, wave, lane);
+  const uint16_t* const k0 = a.k + t.k0 * a.ld_k + (int64_t)kv * D;
+  const uint16_t* const v0 = a.v + t.k0 * a.ld_v + (int64_t)kv * D;
+  auto load = [&](int i) {
+    const int j = key_of(i);
+    rows_in.load(k0 + j * a.ld_k, a.ld_k, t.lk - j, s_k[i & 1], wave);
+    rows_in.load(v0 + j * a.ld_v, a.ld_v, t.lk - j, s_v[i & 1], wave);
+  };
+  if (tiles > 0) load(0);
+
   bf16x8 q[KS], g[KS];
   float delta = 0.f;
   {
@@ -128,20 +144,6 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
     d.stats[(a.q_heads + head) * a.Tq + qrow] = delta;
   }
 
-  const int first = t.first + shift, last = min(t.first + kOwn, t.lq) - 1 + shift;
-  const int in_prefix = (mask.prefix + kPass - 1) / kPass;
-  const int begin = max(mask.lo(first) / kPass, in_prefix);
-  const int tiles = in_prefix + max(0, (mask.hi(last) + kPass - 1) / kPass - begin);
-  auto key_of = [&](int i) { return kPass * (i < in_prefix ? i : i - in_prefix + begin); };
-
-  const RowLoader<DP, kPass, kWaves> rows_in(D, wave, lane);
-  const uint16_t* const k0 = a.k + t.k0 * a.ld_k + (int64_t)kv * D;
-  const uint16_t* const v0 = a.v + t.k0 * a.ld_v + (int64_t)kv * D;
-  auto load = [&](int i) {
-    const int j = key_of(i);
-    rows_in.load(k0 + j * a.ld_k, a.ld_k, t.lk - j, s_k[i & 1], wave);
-    rows_in.load(v0 + j * a.ld_v, a.ld_v, t.lk - j, s_v[i & 1], wave);
-  };
   const bool capped = MORE && a.cap > 0.f, sloped = MORE && a.slopes;
   const float slope2 = sloped ? a.slopes[head] * kLog2e : 0.f;
 
@@ -149,7 +151,6 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
 #pragma unroll
   for (int i = 0; i < DT; ++i) o[i] = zeros16();
 
-  if (tiles > 0) load(0);
   for (int i = 0; i < tiles; ++i) {
     landed();
     if (i + 1 < tiles) load(i + 1);
