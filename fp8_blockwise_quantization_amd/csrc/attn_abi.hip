@@ -82,7 +82,9 @@ fp8rl_status check_heads(int32_t q_heads, int32_t kv_heads, int32_t head_dim, in
 }
 
 fp8rl_status check_scores(float sm_scale, int32_t window, float cap) {
-  if (!isfinite(sm_scale) || !isfinite(cap) || cap < 0.f || window < 0) return FP8RL_ERR_ARG;
+  constexpr float kFar = 0x1p60f;  // their products with log2(e) and with one another stay finite
+  if (!(fabsf(sm_scale) <= kFar) || window < 0) return FP8RL_ERR_ARG;
+  if (cap != 0.f && !(cap >= 1.f / kFar && cap <= kFar)) return FP8RL_ERR_ARG;
   return FP8RL_OK;
 }
 

@@ -49,22 +49,22 @@ struct QueryTiles {
 };
 
 // Products s into scores in units of ln 2, in their places; with a cap, ds times the capped score's slope,
-// 1 - tanh^2 = -4 v (1 + v).
+// 1 - tanh^2.
 template <typename Far>
 __device__ __forceinline__ void finish_scores(f32x16& s, f32x16& ds, const AttnArgs& d, bool capped,
                                               bool sloped, float slope2, Far far) {
   if (capped) {
-    cap_places(s, d);
+    tanh_places<16>(s, d.scale2);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      ds[e] *= -4.f * __builtin_fmaf(s[e], s[e], s[e]);
-      s[e] = __builtin_fmaf(s[e], 2.f * d.cap2, d.cap2);
+      ds[e] *= __builtin_fmaf(-s[e], s[e], 1.f);
+      s[e] *= d.cap2;
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e) s[e] *= d.scale2;
   }
-  if (sloped) slope_scores(s, 1.f, 0.f, slope2, far);
+  if (sloped) slope_scores(s, 1.f, slope2, far);
 }
 
 // Where a wave's lane keeps its part of dk (and behind it dv) of the keys of workgroup `tile`.

@@ -302,10 +302,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
 
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3] * unit;
+      for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3];
       if (capped) {
+        tanh_places<8>(x, unit);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = cap2 * tanh_cap(x[e]);
+        for (int e = 0; e < 8; ++e) x[e] *= cap2;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= unit;
       }
       if (sloped) {
         const float far = (float)(keys.last - 1 - base - 8 * g);

@@ -106,21 +106,20 @@ __global__ __launch_bounds__(256 * KH, 2) void attn_fwd_kernel(AttnArgs d) {
       for (int r = 0; r < NR; ++r)
         s[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kop(32 * r, c), q[c], s[r], 0, 0, 0);
     }
-    // a score in units of ln 2 is mul s + add
-    float mul = d.scale2, add = 0.f;
+    float mul = d.scale2;  // a score in units of ln 2 is mul s
     if (capped) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r) cap_places(s[r], d);
-      mul = 2.f * d.cap2, add = d.cap2;
+      for (int r = 0; r < NR; ++r) tanh_places<16>(s[r], d.scale2);
+      mul = d.cap2;
     }
     if (sloped) {
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const float from = (float)(p - j0 - 32 * r - 4 * h);
-        slope_scores(s[r], mul, add, slope2,
+        slope_scores(s[r], mul, slope2,
                      [&](int e) { return from - (float)(8 * (e >> 2) + (e & 3)); });
       }
-      mul = 1.f, add = 0.f;
+      mul = 1.f;
     }
     if (keys < kOwn || !mask.all(p0, p1, j0, j0 + kOwn)) {
       const int lo = mask.lo(p), hi = mask.hi(p);
@@ -140,7 +139,7 @@ __global__ __launch_bounds__(256 * KH, 2) void attn_fwd_kernel(AttnArgs d) {
     {
       const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top),
                                                       false, false);
-      top = __builtin_fmaf(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), mul, add);
+      top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * mul;
     }
     if (__any(top > m + kRise)) {
       const float was = m;
@@ -150,13 +149,13 @@ __global__ __launch_bounds__(256 * KH, 2) void attn_fwd_kernel(AttnArgs d) {
 #pragma unroll
       for (int c = 0; c < DT; ++c) o[c] *= f;
     }
-    const float shift2 = add - (m == -__builtin_inff() ? 0.f : m);
+    const float ref = m == -__builtin_inff() ? 0.f : m;
     float sum = 0.f;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        s[r][e] = exp2_fast(__builtin_fmaf(s[r][e], mul, shift2));
+        s[r][e] = exp2_fast(__builtin_fmaf(s[r][e], mul, -ref));
         sum += s[r][e];
       }
     l += sum;

@@ -39,10 +39,37 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// tanh of a capped score: 1 - 2 / (e^2x + 1), off by a few 2^-24 (not relative to small x, which is
-// what a score in units of cap needs); exact at both ends, where e^2x is 0 or infinite.
-__device__ __forceinline__ float tanh_cap(float x) {
-  return 1.f - 2.f * __builtin_amdgcn_rcpf(exp2_fast(2.f * kLog2e * x) + 1.f);
+// tanh of N values x = s * scale, in the places of s. Scores are small beside a cap as a rule: up to 1/2 an
+// odd polynomial, fitted to tanh at Chebyshev nodes, is off by 2 units in the last place and takes no longer
+// than 1 - 2 / (exp(2x) + 1), which is off by a few 2^-24 of 1, and so of the cap, however small x is. The
+// latter, exact at both ends, takes over beyond; which it is is decided for the wave.
+template <int N, typename V>
+__device__ __forceinline__ void tanh_places(V& s, float scale) {
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    s[e] *= scale;
+    top = fmaxf(top, fabsf(s[e]));
+  }
+  auto small = [](float x) {
+    const float u = x * x;
+    float f = __builtin_fmaf(u, 0.0179992182f, -0.0533910541f);
+    f = __builtin_fmaf(u, f, 0.133305137f);
+    f = __builtin_fmaf(u, f, -0.333333116f);
+    return __builtin_fmaf(x * u, f, x);
+  };
+  if (!__any(top > 0.5f)) {  // (a NaN stays one on either way)
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e] = small(s[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float x = s[e];
+      const float far = __builtin_fmaf(
+          2.f, __builtin_amdgcn_rcpf(-1.f - exp2_fast(2.f * kLog2e * x)), 1.f);
+      s[e] = fabsf(x) <= 0.5f ? small(x) : far;
+    }
+  }
 }
 
 // Max (sum) over the lanes that differ in bit 4 or 5 of their number, in each of them.

@@ -21,7 +21,7 @@ struct AttnArgs {
   int parts;
   int group;     // query heads of a key head
   int slots;     // tiles of rows, every document's last one counted whole
-  float scale2;  // sm_scale log2(e); capped: 2 sm_scale log2(e) / cap
+  float scale2;  // sm_scale log2(e); capped: sm_scale / cap
   float cap2;    // cap log2(e)
 };
 
@@ -32,7 +32,7 @@ inline AttnArgs attn_args(const fp8rl_attn_args& a, int tile, int64_t T) {
   d.group = a.q_heads / a.kv_heads;
   d.slots = (int)(T / tile + a.docs);
   d.parts = 1;
-  d.scale2 = a.sm_scale * kLog2e * (a.cap > 0.f ? 2.f / a.cap : 1.f);
+  d.scale2 = a.cap > 0.f ? a.sm_scale / a.cap : a.sm_scale * kLog2e;
   d.cap2 = a.cap * kLog2e;
   return d;
 }
@@ -84,20 +84,12 @@ struct Mask {
   }
 };
 
-// A capped score is cap tanh(s / cap) = cap + 2 cap v with v = -1 / (exp(2 s / cap) + 1): of 16
-// products s, v in their places (exact at both ends, where the exponential is 0 or infinite).
-__device__ __forceinline__ void cap_places(f32x16& s, const AttnArgs& d) {
-#pragma unroll
-  for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_rcpf(-1.f - exp2_fast(s[e] * d.scale2));
-}
-// The scores of values v, mul v + add, less slope2 times the distances far(e). Kept apart from the above and
-// from one another, so that the loops stay in one piece under branches that are the same for a call.
+// The scores of values v, mul v, less slope2 times the distances far(e). (Loops of their own, so that they
+// stay in one piece under branches that are the same for a call.)
 template <typename Far>
-__device__ __forceinline__ void slope_scores(f32x16& v, float mul, float add, float slope2, Far far) {
+__device__ __forceinline__ void slope_scores(f32x16& v, float mul, float slope2, Far far) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-    v[e] = __builtin_fmaf(-slope2, fabsf(far(e)),
-                          mul == 1.f && add == 0.f ? v[e] : __builtin_fmaf(v[e], mul, add));
+  for (int e = 0; e < 16; ++e) v[e] = __builtin_fmaf(-slope2, fabsf(far(e)), v[e] * mul);
 }
 
 // ------------------------------------------------------------------------------ rows in LDS

@@ -73,8 +73,8 @@ typedef struct {
  *               may be NULL when that is 0
  * Requires head_dim % 16 == 0, 16 <= head_dim <= 256, 1 <= kv_heads, q_heads a multiple of kv_heads,
  * q_heads <= 4096, B <= 65536, B * kv_heads * ceil(q_heads / kv_heads / 16) < 2^22, page_size >= 1,
- * table_width * page_size <= 2^30, B * table_width * page_size < 2^35, num_pages * page_size < 2^62, sm_scale finite, window >= 0, cap
- * finite and >= 0; bf16 pointers 16-byte and codes 8-byte aligned, pitches and strides multiples of 8
+ * table_width * page_size <= 2^30, B * table_width * page_size < 2^35, num_pages * page_size < 2^62, |sm_scale| <= 2^60, window >= 0, cap
+ * 0 or within 2^-60 .. 2^60; bf16 pointers 16-byte and codes 8-byte aligned, pitches and strides multiples of 8
  * elements, ld_q, ld_out >= the columns, ld_table >= table_width, page_stride (with more than one
  * page), slot_stride and head_stride >= head_dim. B == 0 returns FP8RL_OK.
  */
@@ -159,7 +159,8 @@ typedef struct {
  * Values of v that are NaN or infinite reach rows of their document that do not see them (as 0 * NaN
  * does); they reach no other document.
  * Requires head_dim % 16 == 0, 16 <= head_dim <= 128, 1 <= kv_heads, q_heads a multiple of kv_heads,
- * q_heads <= 4096, Tq, Tk < 2^24, docs < 2^20, sm_scale finite and > 0, window >= 0, cap finite and >= 0;
+ * q_heads <= 4096, Tq, Tk < 2^24, docs < 2^20, 0 < sm_scale <= 2^60, window >= 0, cap 0 or within
+ * 2^-60 .. 2^60;
  * 16-byte aligned rows, pitches multiples of 8 and >= the columns, offsets, prefix, lse and slopes
  * 4-byte aligned. (max(Tq, Tk) / 128 + docs) * q_heads < 2^24, pitches < 2^24.
  * Tq == 0 or docs == 0 returns FP8RL_OK.

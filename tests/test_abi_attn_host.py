@@ -112,9 +112,9 @@ def test_decode_refusals(L):
     assert call(B=65537) == ESHAPE
     assert call(B=65536, table_width=1 << 22, ld_table=1 << 22) == ESHAPE  # 2^42 keys in all
     assert call(B=65536, kv_heads=64, q_heads=64, ld_q=8192, ld_out=8192) == ESHAPE  # 2^22 pieces
-    for v in (NAN, INF, -INF):
+    for v in (NAN, INF, -INF, 1e19):
         assert call(sm_scale=v) == EARG, v
-    for v in (NAN, INF, -1.0):
+    for v in (NAN, INF, -1.0, 1e-19, 1e19):
         assert call(cap=v) == EARG, v
     assert call(window=-1) == EARG
 
@@ -196,9 +196,9 @@ def attention_refusals(call, names, pitches):
     assert call(docs=(1 << 20) - 1, q_heads=20, ld_q=2560, ld_out=2560,
                 ld_dout=2560, ld_dq=2560) == ESHAPE  # 2^24 tiles
     assert call(causal=2) == EARG
-    for v in (NAN, INF, 0.0, -1.0):
+    for v in (NAN, INF, 0.0, -1.0, 1e19):
         assert call(sm_scale=v) == EARG, v
-    for v in (NAN, INF, -1.0):
+    for v in (NAN, INF, -1.0, 1e-19, 1e19):
         assert call(cap=v) == EARG, v
     assert call(window=-1) == EARG
 
