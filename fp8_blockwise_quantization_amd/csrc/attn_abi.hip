@@ -1,4 +1,5 @@
-// C ABI entry points of attention: argument validation (host only, before any HIP call) and dispatch.
+// C ABI entry points of attention: argument validation (host only, before any HIP call) and
+// dispatch.
 #include <math.h>
 #include <stdint.h>
 
@@ -36,8 +37,9 @@ struct Cache {
 
 template <typename Args>
 Cache cache_of(const Args& a) {
-  return {a.k_cache,     a.v_cache,     a.k_scale,  a.v_scale,  a.num_pages,  a.page_size, a.page_stride,
-          a.slot_stride, a.head_stride, a.kv_heads, a.head_dim, a.page_table, a.ld_table,  a.table_width};
+  return {a.k_cache,     a.v_cache,     a.k_scale,     a.v_scale,  a.num_pages,
+          a.page_size,   a.page_stride, a.slot_stride, a.head_stride, a.kv_heads,
+          a.head_dim,    a.page_table,  a.ld_table,    a.table_width};
 }
 
 fp8rl_status check_cache_shape(const Cache& c) {
@@ -162,17 +164,19 @@ namespace {
 
 constexpr int64_t kMaxPitch = int64_t{1} << 24;  // 64 rows are less than 2^32 bytes apart
 
-fp8rl_status check_attn_sizes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_heads, int32_t kv_heads,
-                              int32_t head_dim) {
-  if (Tq < 0 || Tk < 0 || Tq >= (int64_t{1} << 24) || Tk >= (int64_t{1} << 24)) return FP8RL_ERR_SHAPE;
+fp8rl_status check_attn_sizes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_heads,
+                              int32_t kv_heads, int32_t head_dim, int32_t widest) {
+  constexpr int64_t kRows = int64_t{1} << 24;
+  if (Tq < 0 || Tk < 0 || Tq >= kRows || Tk >= kRows) return FP8RL_ERR_SHAPE;
   if (docs < 0 || docs >= (int64_t{1} << 20)) return FP8RL_ERR_SHAPE;
-  if (fp8rl_status s = check_heads(q_heads, kv_heads, head_dim, 128)) return s;
+  if (fp8rl_status s = check_heads(q_heads, kv_heads, head_dim, widest)) return s;
   if (((Tq > Tk ? Tq : Tk) / 128 + docs) * q_heads >= (int64_t{1} << 24)) return FP8RL_ERR_SHAPE;
   return FP8RL_OK;
 }
 
-fp8rl_status check_attn_shape(const fp8rl_attn_args& a) {
-  if (fp8rl_status s = check_attn_sizes(a.Tq, a.Tk, a.docs, a.q_heads, a.kv_heads, a.head_dim))
+fp8rl_status check_attn_shape(const fp8rl_attn_args& a, int32_t widest) {
+  if (fp8rl_status s =
+          check_attn_sizes(a.Tq, a.Tk, a.docs, a.q_heads, a.kv_heads, a.head_dim, widest))
     return s;
   if (a.causal != 0 && a.causal != 1) return FP8RL_ERR_ARG;
   if (fp8rl_status s = check_scores(a.sm_scale, a.window, a.cap)) return s;
@@ -205,7 +209,7 @@ fp8rl_status check_attn_inputs(const fp8rl_attn_args& a) {
 fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream) {
   if (!args) return FP8RL_ERR_NULL;
   const fp8rl_attn_args& a = *args;
-  if (fp8rl_status s = check_attn_shape(a)) return s;
+  if (fp8rl_status s = check_attn_shape(a, 256)) return s;
   if (a.Tq == 0 || a.docs == 0) return FP8RL_OK;
   if (fp8rl_status s = check_attn_inputs(a)) return s;
   return hip_status(fp8rl::launch_attn_fwd(a, as_stream(stream)));
@@ -213,7 +217,7 @@ fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream) {
 
 size_t fp8rl_attn_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_heads,
                                       int32_t kv_heads, int32_t head_dim) {
-  if (check_attn_sizes(Tq, Tk, docs, q_heads, kv_heads, head_dim) != FP8RL_OK) return 0;
+  if (check_attn_sizes(Tq, Tk, docs, q_heads, kv_heads, head_dim, 128) != FP8RL_OK) return 0;
   return fp8rl::attn_bwd_workspace(Tq, Tk, docs, q_heads, kv_heads, head_dim);
 }
 
@@ -221,7 +225,7 @@ fp8rl_status fp8rl_attn_bwd(const fp8rl_attn_args* args, void* workspace, size_t
                             void* stream) {
   if (!args) return FP8RL_ERR_NULL;
   const fp8rl_attn_args& a = *args;
-  if (fp8rl_status s = check_attn_shape(a)) return s;
+  if (fp8rl_status s = check_attn_shape(a, 128)) return s;
   if ((a.Tq == 0 && a.Tk == 0) || a.docs == 0) return FP8RL_OK;
   const int64_t qc = (int64_t)a.q_heads * a.head_dim, kc = (int64_t)a.kv_heads * a.head_dim;
   if (!a.q_offsets || !a.k_offsets) return FP8RL_ERR_NULL;

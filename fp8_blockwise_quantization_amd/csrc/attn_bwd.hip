@@ -1,12 +1,12 @@
-// Gradients of attention of packed documents: two passes over the scores, one for dq (a query's sums
-// stay in one workgroup) and one for dk and dv (a key's do), so that nothing is added atomically
-// and the result has the same bits every time. Seven products instead of the five that one
-// pass with atomic sums would need.
+// Gradients of attention of packed documents: two passes over the scores, one for dq (a query's
+// sums stay in one workgroup) and one for dk and dv (a key's do), so that nothing is added
+// atomically and the result has the same bits every time. Seven products instead of the five that
+// one pass with atomic sums would need.
 //
 // dq: as the forward pass, 128 queries a workgroup, queries in the columns. Per tile of 64 keys
 //   S^T = K Q^T,  dP^T = V dO^T,  P = exp(S - lse),  dS = P (dP - delta),  dQ^T += K^T dS^T,
-// where delta = <dout, out> of a query, formed first and left in the workspace (with lse in units of ln 2)
-// for the second pass.
+// where delta = <dout, out> of a query, formed first and left in the workspace (with lse in units
+// of ln 2) for the second pass.
 //
 // dk, dv: 128 keys a workgroup, keys in the columns, through the tiles of 64 queries of all heads
 // that share the keys:
@@ -48,8 +48,8 @@ struct QueryTiles {
   }
 };
 
-// Products s into scores in units of ln 2, in their places; with a cap, ds times the capped score's slope,
-// 1 - tanh^2.
+// Products s into scores in units of ln 2, in their places; with a cap, ds times the capped score's
+// slope, 1 - tanh^2.
 template <typename Far>
 __device__ __forceinline__ void finish_scores(f32x16& s, f32x16& ds, const AttnArgs& d, bool capped,
                                               bool sloped, float slope2, Far far) {
@@ -404,8 +404,8 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnArgs d) {
   }
 }
 
-// The parts of dk and dv of a workgroup's keys, added in order: a wave per 32 keys and 32 columns of
-// either.
+// The parts of dk and dv of a workgroup's keys, added in order: a wave per 32 keys and 32 columns
+// of either.
 template <int DP>
 __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs d) {
   constexpr int DT = DP / 32;
@@ -439,8 +439,9 @@ __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs d) {
 
 namespace {
 
-// Parts that a key tile's queries are dealt out in: enough workgroups for two to a CU. (What splitting
-// costs is the parts' way through memory, 8 bytes a value of dk and dv and part, each way.)
+// Parts that a key tile's queries are dealt out in: enough workgroups for two to a CU. (What
+// splitting costs is the parts' way through memory, 8 bytes a value of dk and dv and part, each
+// way.)
 int key_parts(int64_t Tk, int64_t docs, int kv_heads) {
   const int64_t tiles = (Tk / kOwn + docs) * kv_heads;
   return (int)max((int64_t)1, min((int64_t)kMostParts, 512 / max((int64_t)1, tiles)));

@@ -1,7 +1,7 @@
 // Attention of one query per sequence over a paged cache, split over the cache's length and joined.
 //
-// With the running maximum m of a head's scores, its sum l = sum exp(a - m) and o = sum exp(a - m) v,
-// a tile of keys updates the three; parts of a sequence meet as
+// With the running maximum m of a head's scores, its sum l = sum exp(a - m) and o = sum exp(a - m)
+// v, a tile of keys updates the three; parts of a sequence meet as
 //   M = max m_i,  l = sum l_i 2^(m_i - M),  o = sum o_i 2^(m_i - M)      (scores in units of ln 2).
 //
 // A wave, one of eight, takes 32 keys at a time, for up to 16 query heads that share them:
@@ -28,12 +28,16 @@ constexpr int kWhole = 512; // keys up to which a sequence is not split
 constexpr int kLeast = 2;   // units of a piece
 
 // Who does what.
-//   Where no sequence has more than kWhole keys, a workgroup takes a sequence and head tile, its waves
+//   Where no sequence has more than kWhole keys, a workgroup takes a sequence and head tile, its
+//   waves
 //   the sequence's units in turn; their parts meet in LDS, and that is all.
-//   Else a wave takes a head tile and a piece of all sequences' units in a row. As many waves as run
+//   Else a wave takes a head tile and a piece of all sequences' units in a row. As many waves as
+//   run
 //   at once all take the same number of units, however the lengths differ; a wave may so end one
-//   sequence, take others whole and begin a last one. What it has of a sequence that was cut goes to
-//   memory, and a second kernel joins it. The waves of a workgroup have neighbouring heads of the same
+//   sequence, take others whole and begin a last one. What it has of a sequence that was cut goes
+//   to
+//   memory, and a second kernel joins it. The waves of a workgroup have neighbouring heads of the
+//   same
 //   keys, which a cache laid out by tokens has side by side.
 struct DecodeArgs {
   fp8rl_attn_decode_args a;
@@ -98,9 +102,9 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& d, int lot, int b,
   return {B, base, per};
 }
 
-// N 32-bit words at p, which is aligned to 8 bytes (4 for one word). ONCE: not kept in the caches (for
-// v, whose lines an instruction takes whole: 57.8 -> 53.8 us at 64 x 4096; k's come half a line at a time,
-// and some were read twice).
+// N 32-bit words at p, which is aligned to 8 bytes (4 for one word). ONCE: not kept in the caches
+// (for v, whose lines an instruction takes whole: 57.8 -> 53.8 us at 64 x 4096; k's come half a
+// line at a time, and some were read twice).
 template <bool ONCE, int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
   typedef u32x4 __attribute__((aligned(8))) u32x4_8;
@@ -126,8 +130,8 @@ __device__ __forceinline__ uint32_t halves(uint32_t a, uint32_t b, bool high) {
 
 }  // namespace
 
-// DP: head_dim rounded up to 64, 128 or 256; PAD: it is less. CODES: an E4M3 cache. SPLIT: pieces to
-// waves.
+// DP: head_dim rounded up to 64, 128 or 256; PAD: it is less. CODES: an E4M3 cache. SPLIT: pieces
+// to waves.
 template <int DP, bool PAD, bool CODES, bool SPLIT>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs d) {
   constexpr int VW = DP / 16;                   // columns of v a lane holds
@@ -137,7 +141,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
   constexpr int OS = DP + 4;
   constexpr int kStep = SPLIT ? kUnit : kUnit * kWaves;
   __shared__ int64_t s_at[kWaves][2][32];
-  __shared__ float s_o[SPLIT ? 1 : kWaves][SPLIT ? 1 : 16][SPLIT ? 1 : OS];
+  __shared__ float s_o[kWaves][16][OS];  // (of no use, and so not there, with SPLIT)
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   const fp8rl_attn_decode_args& a = d.a;
   const int lane = (int)(threadIdx.x & 63);
@@ -421,7 +425,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int t = 0; t < VW; ++t) s_o[SPLIT ? 0 : wave][SPLIT ? 0 : col][SPLIT ? 0 : (4 * g + i) * VW + t] = o[t][i];
+      for (int t = 0; t < VW; ++t) s_o[wave][col][(4 * g + i) * VW + t] = o[t][i];
     }
     __syncthreads();
     const int pairs = D / 2;
@@ -435,8 +439,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
       for (int i = 0; i < kWaves; ++i) {
         // (a wave that saw no key has zeros; one that saw a NaN is not left out)
         const float li = s_l[i][h], f = li == 0.f ? 0.f : exp2_fast(s_m[i][h] - top);
-        const float2 v = *reinterpret_cast<const float2*>(
-            &s_o[SPLIT ? 0 : i][SPLIT ? 0 : h][SPLIT ? 0 : at]);
+        const float2 v = *reinterpret_cast<const float2*>(&s_o[i][h][at]);
         sum += li * f;
         x += v.x * f;
         y += v.y * f;
@@ -449,7 +452,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
   }
 }
 
-// The parts of a sequence that was cut, for one query head. W waves share the parts, and then their sums.
+// The parts of a sequence that was cut, for one query head. W waves share the parts, and then their
+// sums.
 template <int W>
 __global__ __launch_bounds__(W > 1 ? 64 * W : 256) void attn_decode_join_kernel(DecodeArgs d) {
   constexpr int kItems = W > 1 ? 1 : 4;  // of a workgroup
@@ -571,8 +575,8 @@ hipError_t launch_attn_decode(const fp8rl_attn_decode_args& a, void* workspace, 
     return hipGetLastError();
   }
   a.k_scale ? run_decode<true, true>(d, stream) : run_decode<false, true>(d, stream);
-  // a wave has sixteen of a sequence's parts in flight at a time; where there are more, eight waves share
-  // them
+  // a wave has sixteen of a sequence's parts in flight at a time; where there are more, eight waves
+  // share them
   const int64_t items = a.B * a.q_heads;
   if (d.lots <= 16 * a.B)
     hipLaunchKernelGGL(attn_decode_join_kernel<1>, dim3((unsigned)((items + 3) / 4)), dim3(256), 0,

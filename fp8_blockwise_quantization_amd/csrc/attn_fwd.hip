@@ -1,8 +1,8 @@
 // Attention of packed documents.
 //
-// A workgroup has 128 queries of one head of a document, 32 a wave, and goes through the 64-key tiles that
-// any of them sees; keys and values reach LDS two tiles deep by direct loads. Per tile, with the
-// queries in the columns of the matrix instruction:
+// A workgroup has 128 queries of one head of a document, 32 a wave, and goes through the 64-key
+// tiles that any of them sees; keys and values reach LDS two tiles deep by direct loads. Per tile,
+// with the queries in the columns of the matrix instruction:
 //   S^T = K Q^T,   m = max(m, max S),   P = exp(S - m),   l += sum P,   O^T += V^T P^T,
 // so that a query's statistics are in the two lanes that hold its column, and P^T goes from one
 // product into the other in its registers (attn_tile.hpp). V^T is read out of V's rows by
@@ -20,8 +20,8 @@ constexpr int kFew = 512;  // workgroups up to which two waves share the keys
 
 }  // namespace
 
-// DP: head_dim rounded up to 64 or 128; PAD: it is less. MORE: capped scores or slopes. KH: waves that
-// share 32 queries, each with its part of a tile's keys; their sums meet in the end.
+// DP: head_dim rounded up to 64 or 128; PAD: it is less. MORE: capped scores or slopes. KH: waves
+// that share 32 queries, each with its part of a tile's keys; their sums meet in the end.
 template <int DP, bool PAD, bool MORE, int KH>
 __global__ __launch_bounds__(256 * KH, 2) void attn_fwd_kernel(AttnArgs d) {
   constexpr int KS = DP / 16, DT = DP / 32;
@@ -35,8 +35,8 @@ __global__ __launch_bounds__(256 * KH, 2) void attn_fwd_kernel(AttnArgs d) {
   const int block = wave & 3, part = wave >> 2;  // of the queries, of a tile's keys
   const int D = PAD ? a.head_dim : DP;
 
-  // key heads fastest (with 8 of them, one to an XCD and its L2), the last tiles of documents, which
-  // see the most keys, first
+  // key heads fastest (with 8 of them, one to an XCD and its L2), the last tiles of documents,
+  // which see the most keys, first
   const int id = (int)blockIdx.x;
   const int kv = id % a.kv_heads;
   const int head = kv * d.group + id / a.kv_heads % d.group;
@@ -233,7 +233,14 @@ hipError_t launch_attn_fwd(const fp8rl_attn_args& a, hipStream_t stream) {
   else if (a.head_dim < 64)
     more ? go(attn_fwd_kernel<64, true, true, 1>, attn_fwd_kernel<64, true, true, 2>)
          : go(attn_fwd_kernel<64, true, false, 1>, attn_fwd_kernel<64, true, false, 2>);
-  else if (a.head_dim < 128)
+  else if (a.head_dim > 128) {
+    // 32 queries of 256 columns and their sums take a wave's registers without a second part of keys
+    auto wide = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(512), 0, stream, d); };
+    if (a.head_dim == 256)
+      more ? wide(attn_fwd_kernel<256, false, true, 2>) : wide(attn_fwd_kernel<256, false, false, 2>);
+    else
+      more ? wide(attn_fwd_kernel<256, true, true, 2>) : wide(attn_fwd_kernel<256, true, false, 2>);
+  } else if (a.head_dim < 128)
     more ? go(attn_fwd_kernel<128, true, true, 1>, attn_fwd_kernel<128, true, true, 2>)
          : go(attn_fwd_kernel<128, true, false, 1>, attn_fwd_kernel<128, true, false, 2>);
   else

@@ -39,10 +39,11 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// tanh of N values x = s * scale, in the places of s. Scores are small beside a cap as a rule: up to 1/2 an
-// odd polynomial, fitted to tanh at Chebyshev nodes, is off by 2 units in the last place and takes no longer
-// than 1 - 2 / (exp(2x) + 1), which is off by a few 2^-24 of 1, and so of the cap, however small x is. The
-// latter, exact at both ends, takes over beyond; which it is is decided for the wave.
+// tanh of N values x = s * scale, in the places of s. Scores are small beside a cap as a rule: up
+// to 1/2 an odd polynomial, fitted to tanh at Chebyshev nodes, is off by 2 units in the last place
+// and takes no longer than 1 - 2 / (exp(2x) + 1), which is off by a few 2^-24 of 1, and so of the
+// cap, however small x is. The latter, exact at both ends, takes over beyond; which it is is
+// decided for the wave.
 template <int N, typename V>
 __device__ __forceinline__ void tanh_places(V& s, float scale) {
   float top = 0.f;
@@ -97,7 +98,8 @@ __device__ __forceinline__ u32x2 codes_f16(uint32_t w) {
 }
 
 // The page that holds a key: key / page_size by a product with ceil(2^62 / page_size), exact for
-// keys and page sizes below 2^31 (the product's error, key * (page_size - 1) at most, is below 2^62).
+// keys and page sizes below 2^31 (the product's error, key * (page_size - 1) at most, is below
+// 2^62).
 struct PageOf {
   uint64_t reciprocal;
   int page_size;

@@ -1,12 +1,12 @@
 // What the kernels over packed documents share: documents and masks, tiles of rows in LDS, and the
 // operands of the 32x32x16 matrix instruction.
 //
-// The instruction's layouts (lane l, h = l / 32): operand A holds row l % 32, operand B column l % 32,
-// each at the 8 places 8h .. 8h + 7 of the contraction; the result's column is l % 32, its rows are
-// 8 (i / 4) + 4h + i % 4 for i = 0 .. 15. The rows that a lane has of a result, eight by eight, serve
-// as the places of the next contraction (16 of them: 16s + {4h .. 4h + 3, 8 + 4h .. 8 + 4h + 3}), so a
-// result turns into an operand without leaving the lane, as long as the other operand takes its
-// places in the same order: operand_t does.
+// The instruction's layouts (lane l, h = l / 32): operand A holds row l % 32, operand B column l %
+// 32, each at the 8 places 8h .. 8h + 7 of the contraction; the result's column is l % 32, its rows
+// are 8 (i / 4) + 4h + i % 4 for i = 0 .. 15. The rows that a lane has of a result, eight by eight,
+// serve as the places of the next contraction (16 of them: 16s + {4h .. 4h + 3, 8 + 4h .. 8 + 4h +
+// 3}), so a result turns into an operand without leaving the lane, as long as the other operand
+// takes its places in the same order: operand_t does.
 #pragma once
 
 #include "attn_ops.hpp"
@@ -84,8 +84,8 @@ struct Mask {
   }
 };
 
-// The scores of values v, mul v, less slope2 times the distances far(e). (Loops of their own, so that they
-// stay in one piece under branches that are the same for a call.)
+// The scores of values v, mul v, less slope2 times the distances far(e). (Loops of their own, so
+// that they stay in one piece under branches that are the same for a call.)
 template <typename Far>
 __device__ __forceinline__ void slope_scores(f32x16& v, float mul, float slope2, Far far) {
 #pragma unroll
@@ -112,8 +112,8 @@ __device__ __forceinline__ const void* scalar_ptr(const void* p) {
 
 // 16 bytes a lane from base + off (base the same in all lanes) to lds + 16 * lane, past the
 // registers. In assembly because the compiler would wait for every such load in flight before any
-// read of LDS; landed() waits instead. The address may come from v_readfirstlane right before, which
-// needs 5 wait states, and M0 needs 1.
+// read of LDS; landed() waits instead. The address may come from v_readfirstlane right before,
+// which needs 5 wait states, and M0 needs 1.
 __device__ __forceinline__ void dma_rows(const void* base, uint32_t off, const void* lds) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds);
   asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1"
@@ -127,7 +127,8 @@ __device__ __forceinline__ void dma_floats(const void* base, uint32_t off, const
                :: "v"(off), "s"(scalar_ptr(base)), "{m0}"(m0) : "memory");
 }
 
-// This wave's loads but the last N have arrived and its reads of LDS are done, and so with the others.
+// This wave's loads but the last N have arrived and its reads of LDS are done, and so with the
+// others.
 template <int N = 0>
 __device__ __forceinline__ void landed() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -226,9 +227,9 @@ __device__ __forceinline__ bf16x8 row_operand(const uint16_t* row, int s, int h,
   return __builtin_bit_cast(bf16x8, t);
 }
 
-// A result with a row of the matrix in each column (lane l: row l % 32, columns c0 + 8 (i / 4) + 4h +
-// i % 4), times f, rounded and stored where `in`: 16 bytes a lane after the two halves of the wave have
-// exchanged every other four.
+// A result with a row of the matrix in each column (lane l: row l % 32, columns c0 + 8 (i / 4) + 4h
+// + i % 4), times f, rounded and stored where `in`: 16 bytes a lane after the two halves of the
+// wave have exchanged every other four.
 __device__ __forceinline__ void store_columns(const f32x16& v, float f, uint16_t* row, int c0, int h,
                                               int head_dim, bool in) {
 #pragma unroll

@@ -33,9 +33,14 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs r) {
     int b = last_not_past((int)a.B, row0, lane, [&](int i) { return a.offsets[i]; });
     const int row = row0 + lane;
     if (lane < kRows && row < a.R) {
-      while (b < (int)a.B && a.offsets[b + 1] <= row) ++b;
+      // the row's sequence: as a rule row0's, else past that in doubling steps
+      auto past = [&](int i) { return i <= (int)a.B && a.offsets[i] <= row; };
+      int step = 1;
+      for (; past(b + step); step *= 2) b += step;
+      for (; step > 0; step /= 2)
+        if (past(b + step)) b += step;
       if (b < (int)a.B && a.offsets[b] <= row) {
-        const int64_t key = (int64_t)(row - a.offsets[b]) + (a.starts ? a.starts[b] : 0);
+        const int64_t key = (int64_t)row - a.offsets[b] + (a.starts ? a.starts[b] : 0);
         if (key >= 0 && key < (int64_t)a.table_width * a.page_size) {
           const int i = r.page_of((int)key);
           const int page = a.page_table[b * a.ld_table + i];
@@ -67,8 +72,10 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs r) {
                                                         src[i] + at);
         k[i].x = x.x, k[i].y = x.y, v[i].x = y.x, v[i].y = y.y;
       } else {
-        k[i] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.k_cache) + src[i] + at);
-        v[i] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.v_cache) + src[i] + at);
+        k[i] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.k_cache) + src[i] +
+                                               at);
+        v[i] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.v_cache) + src[i] +
+                                               at);
       }
     }
     auto widen = [](u32x4 w, float s) {

@@ -173,7 +173,7 @@ DOCS = dict(q=A, k=A, v=A, ld_q=512, ld_k=256, ld_v=256, Tq=100, Tk=120, q_heads
             ld_dq=512, ld_dk=256, ld_dv=256)
 
 
-def attention_refusals(call, names, pitches):
+def attention_refusals(call, names, pitches, wide):
     for n in names:
         assert call(**{n: None}) == ENULL, n
     for n in names:
@@ -185,7 +185,7 @@ def attention_refusals(call, names, pitches):
         assert call(**{n: DOCS[n] - 8}) == ESHAPE, n
         assert call(**{n: DOCS[n] + 4}) == EALIGN, n
         assert call(**{n: 1 << 24}) == ESHAPE, n
-    for d in (0, 8, 40, 144):
+    for d in (0, 8, 40, wide):
         assert call(head_dim=d) == ESHAPE, d
     for h in (0, -4, 1, 3, 4098):
         assert call(q_heads=h) == ESHAPE, h
@@ -211,7 +211,7 @@ def test_fwd_refusals(L):
     assert call(Tq=0, q=None, out=None) == OK
     assert call(docs=0, q_offsets=None) == OK
     attention_refusals(call, ("q", "k", "v", "out", "q_offsets", "k_offsets"),
-                       ("ld_q", "ld_k", "ld_v", "ld_out"))
+                       ("ld_q", "ld_k", "ld_v", "ld_out"), wide=272)
 
 
 def test_bwd_refusals(L):
@@ -230,7 +230,8 @@ def test_bwd_refusals(L):
     assert call(docs=0, q_offsets=None) == OK
     attention_refusals(call, ("q", "k", "v", "out", "q_offsets", "k_offsets", "lse", "dout", "dq", "dk",
                               "dv"),
-                       ("ld_q", "ld_k", "ld_v", "ld_out", "ld_dout", "ld_dq", "ld_dk", "ld_dv"))
+                       ("ld_q", "ld_k", "ld_v", "ld_out", "ld_dout", "ld_dq", "ld_dk", "ld_dv"),
+                       wide=144)
     assert call(Tk=0, k=None, dk=None, dq=None) == ENULL
     assert call(Tq=0, q=None, dq=None, dv=None) == ENULL
     assert call(ws=None) == EWS

@@ -181,6 +181,16 @@ def test_head_widths(D, more):
     check_bwd(d)
 
 
+@pytest.mark.parametrize("D", [144, 192, 240, 256])
+@pytest.mark.parametrize("more", [{}, dict(cap=3.0, slopes=True, window=70, prefix=[0, 9, 3])])
+def test_wide_heads(D, more):
+    """Forward alone: the gradients end at 128 columns."""
+    d = Docs([1, 77, 290], D=D, Hq=2, Hkv=1, seed=D, **more)
+    out, lse = check_fwd(d)
+    with pytest.raises(fq.Fp8rlError):
+        fq.attn_bwd(d.dout.cuda(), *d.dev, out, lse, D, d.q_offsets, **d.args)
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (7, 1), (6, 2), (16, 8)])
 def test_groups(Hq, Hkv):
     d = Docs([70, 140], Hq=Hq, Hkv=Hkv, seed=Hq, fused=True)
