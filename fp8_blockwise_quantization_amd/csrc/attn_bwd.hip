@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
   const int id = (int)blockIdx.x;  // (the order is the forward pass's)
   const int kv = id % a.kv_heads;
   const int head = kv * d.group + id / a.kv_heads % d.group;
-  const DocTile t = find_tile<kOwn, false>(a, d.slots - 1 - id / a.q_heads, lane);
+  const DocTile t = find_tile<kOwn, false>(d, id / a.q_heads, lane);
   if (t.doc >= (int)a.docs) return;
   const Mask mask(a, t);
   const int shift = t.lk - t.lq;
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnArgs d) {
   const int id = (int)blockIdx.x;
   const int kv = id % a.kv_heads;
   const int part = id / a.kv_heads % d.parts;
-  const DocTile t = find_tile<kOwn, true>(a, id / (a.kv_heads * d.parts), lane);
+  const DocTile t = find_tile<kOwn, true>(d, id / (a.kv_heads * d.parts), lane);
   if (t.doc >= (int)a.docs) return;
   const Mask mask(a, t);
   const int shift = t.lk - t.lq;
@@ -421,7 +421,7 @@ __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs d) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[part][e] = from[64 * e];
   }
-  const DocTile t = find_tile<kOwn, true>(a, (int)blockIdx.x / a.kv_heads, lane);
+  const DocTile t = find_tile<kOwn, true>(d, (int)blockIdx.x / a.kv_heads, lane);
   const int key = t.first + 32 * wave;
   if (t.doc >= (int)a.docs || key >= t.lk) return;
   f32x16 g = zeros16();
@@ -444,7 +444,7 @@ namespace {
 // way.)
 int key_parts(int64_t Tk, int64_t docs, int kv_heads) {
   const int64_t tiles = (Tk / kOwn + docs) * kv_heads;
-  return (int)max((int64_t)1, min((int64_t)kMostParts, 512 / max((int64_t)1, tiles)));
+  return (int)max((int64_t)1, min((int64_t)kMostParts, 640 / max((int64_t)1, tiles)));
 }
 
 int padded(int head_dim) { return head_dim <= 64 ? 64 : 128; }

@@ -64,17 +64,6 @@ __device__ __forceinline__ Keys keys_of(const DecodeArgs& d, int b) {
   return k;
 }
 
-// Sums over the lanes up to each.
-__device__ __forceinline__ int sum_upto(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
-  return v;
-}
-
 // A sequence's place among all sequences' units, and what a wave takes of these.
 struct Place {
   int b, before;  // sequence and the units in front of it

@@ -35,12 +35,11 @@ __global__ __launch_bounds__(256 * KH, 2) void attn_fwd_kernel(AttnArgs d) {
   const int block = wave & 3, part = wave >> 2;  // of the queries, of a tile's keys
   const int D = PAD ? a.head_dim : DP;
 
-  // key heads fastest (with 8 of them, one to an XCD and its L2), the last tiles of documents,
-  // which see the most keys, first
+  // key heads fastest: with 8 of them, one to an XCD and its L2
   const int id = (int)blockIdx.x;
   const int kv = id % a.kv_heads;
   const int head = kv * d.group + id / a.kv_heads % d.group;
-  const DocTile t = find_tile<kQ, false>(a, d.slots - 1 - id / a.q_heads, lane);
+  const DocTile t = find_tile<kQ, false>(d, id / a.q_heads, lane);
   if (t.doc >= (int)a.docs) return;
   const Mask mask(a, t);
   const int shift = t.lk - t.lq;

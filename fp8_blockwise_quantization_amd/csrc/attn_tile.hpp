@@ -37,30 +37,73 @@ inline AttnArgs attn_args(const fp8rl_attn_args& a, int tile, int64_t T) {
   return d;
 }
 
-// A tile of BM rows of a document. Documents in order take
-//   rows[d + 1] / BM + d + 1 - (rows[d] / BM + d)  >=  ceil(length / BM)
-// tiles each, so that tile `slot` is found from the offsets alone.
+// A tile of BM rows of a document: of its queries, or with KEYS of its keys.
 struct DocTile {
-  int doc;        // docs: none
-  int first;      // the tile's first row in the document
-  int lq, lk;     // queries and keys of the document
-  int64_t q0, k0; // its first row of q, of k and v
+  int doc;         // docs: none
+  int first;       // the tile's first row in the document
+  int lq, lk;      // queries and keys of the document
+  int64_t q0, k0;  // its first row of q, of k and v
 };
 
+// The tile that comes at place `index` of the launch's a.slots.
+//
+// Up to 64 documents: tiles that take longest first, so that the last ones to run are short. A tile
+// of queries goes through the keys in front of it, one of keys through the queries behind it; with
+// `weight` the number of these tiles of the other kind less those that the tile's own place adds,
+// a document has a tile of each weight + 0 .. weight + tiles - 1 (not causal: all of the same). How
+// many tiles there are of at least k is a sum over the documents, one to a lane, and k is found by
+// its bits.
+//
+// More documents: from the last (with KEYS the first) document's on. Documents take
+//   rows[d + 1] / BM + d + 1 - (rows[d] / BM + d)  >=  ceil(length / BM)
+// places each, so that a tile is found from the offsets alone.
 template <int BM, bool KEYS>
-__device__ __forceinline__ DocTile find_tile(const fp8rl_attn_args& a, int slot, int lane) {
+__device__ __forceinline__ DocTile find_tile(const AttnArgs& args, int index, int lane) {
+  const fp8rl_attn_args& a = args.a;
   const int n = (int)a.docs, Tq = (int)a.Tq, Tk = (int)a.Tk;
   auto q_at = [&](int i) { return min(max(a.q_offsets[i], 0), Tq); };
   auto k_at = [&](int i) { return min(max(a.k_offsets[i], 0), Tk); };
   DocTile t;
-  t.doc = last_not_past(n, slot, lane,
-                        [&](int i) { return (KEYS ? k_at(i) : q_at(i)) / BM + i; });
-  if (t.doc >= n) return t;
-  t.q0 = q_at(t.doc), t.k0 = k_at(t.doc);
-  t.lq = max(0, q_at(t.doc + 1) - (int)t.q0);
-  t.lk = max(0, k_at(t.doc + 1) - (int)t.k0);
-  t.first = (slot - ((int)(KEYS ? t.k0 : t.q0) / BM + t.doc)) * BM;
-  if (t.first < 0 || t.first >= (KEYS ? t.lk : t.lq)) t.doc = n;
+  t.doc = n;
+  if (n <= 64) {
+    int q0 = 0, k0 = 0, lq = 0, lk = 0;
+    if (lane < n) {
+      q0 = q_at(lane), k0 = k_at(lane);
+      lq = max(0, q_at(lane + 1) - q0), lk = max(0, k_at(lane + 1) - k0);
+    }
+    const int own = KEYS ? lk : lq, other = KEYS ? lq : lk;
+    const int tiles = (own + BM - 1) / BM;
+    const int weight = (a.causal ? max(0, other - own) : other) / BM;
+    // tiles of at least k
+    auto heavy = [&](int k) {
+      return a.causal ? min(max(tiles + weight - k, 0), tiles) : weight >= k ? tiles : 0;
+    };
+    auto all_heavy = [&](int k) { return __builtin_amdgcn_readlane(sum_upto(heavy(k)), 63); };
+    if (index >= all_heavy(0)) return t;
+    int bit = 1, k = 0;
+    while (__ballot(tiles + weight >= bit)) bit *= 2;
+    for (; bit > 0; bit /= 2)
+      if (index < all_heavy(k + bit)) k += bit;
+    const int rest = index - all_heavy(k + 1);
+    const int mine = heavy(k) - heavy(k + 1);
+    const int upto = sum_upto(mine);
+    const int d = __builtin_ctzll(__ballot(upto > rest));
+    const int at = a.causal ? k - weight : rest - (upto - mine);
+    t.doc = d;
+    t.first = BM * __builtin_amdgcn_readlane(KEYS && a.causal ? tiles - 1 - at : at, d);
+    t.q0 = __builtin_amdgcn_readlane(q0, d), t.k0 = __builtin_amdgcn_readlane(k0, d);
+    t.lq = __builtin_amdgcn_readlane(lq, d), t.lk = __builtin_amdgcn_readlane(lk, d);
+    return t;
+  }
+  const int slot = KEYS ? index : args.slots - 1 - index;
+  const int d =
+      last_not_past(n, slot, lane, [&](int i) { return (KEYS ? k_at(i) : q_at(i)) / BM + i; });
+  if (d >= n) return t;
+  t.q0 = q_at(d), t.k0 = k_at(d);
+  t.lq = max(0, q_at(d + 1) - (int)t.q0);
+  t.lk = max(0, k_at(d + 1) - (int)t.k0);
+  t.first = (slot - ((int)(KEYS ? t.k0 : t.q0) / BM + d)) * BM;
+  if (t.first >= 0 && t.first < (KEYS ? t.lk : t.lq)) t.doc = d;
   return t;
 }
 
