@@ -16,6 +16,16 @@
 //
 // The cache's rows are found through the page table: lane i resolves key i of the next tile while
 // the present one is worked on, and hands the 64-bit offset out through LDS.
+//
+// Bound by memory; every key and value is read once. Values go past the caches (nontemporal loads:
+// 64 uneven sequences of up to 4096 keys of 8 heads of 128 in E4M3, 57.8 us without, 53.1 with),
+// keys do not (their rows are read 64 bytes at a time, and the other half of a line was gone by the
+// next step: 35 us instead of 32 for a window of 1024 keys of 256). Those 64 sequences are 246 MB:
+// 49 us for this kernel, 5.0 TB/s, and 6 for the join; 529 MB, eight uneven sequences of up to
+// 32768 keys of 4 heads of 128 in bf16: 88 us, 6.0 TB/s, and 6. What lies beside the bytes is the
+// launch and the chain of lengths, table and first keys, about 4 us. Two tiles of keys under way in
+// a wave (59.9 against 57.4 us: 16 waves' registers become 8's) and sixteen waves a CU with half a
+// piece each (69) were slower.
 #include "attn_ops.hpp"
 
 namespace fp8rl {
@@ -24,21 +34,23 @@ namespace {
 
 constexpr int kWaves = 8;   // of a workgroup, and what a CU runs at once
 constexpr int kUnit = 32;   // keys of a wave's step
-constexpr int kWhole = 512; // keys up to which a sequence is not split
+// Keys, and their bytes in a head, up to which a sequence is not split. Uneven sequences of 32
+// query heads on 8 of 128 in E4M3, up to 1020 keys each, not split and split: one 9.8 and 13.0 us,
+// 64 of them 20.4 and 25.7; up to 1500 12.6 and 13.0, 27.7 and 29.8; up to 2040 16.6 and 13.2, both
+// 36. 1024 keys each of 8 heads of 256, one sequence and 100: in E4M3 16.2 and 17.3, 83.2 and 81.5;
+// in bf16 (twice these bytes) 38.8 and 29.2, 207 and 164.
+constexpr int kWhole = 1024;
+constexpr int kWholeBytes = 256 << 10;
 constexpr int kLeast = 2;   // units of a piece
 
 // Who does what.
-//   Where no sequence has more than kWhole keys, a workgroup takes a sequence and head tile, its
-//   waves
+//   Where all sequences are short (kWhole), a workgroup takes a sequence and head tile, its waves
 //   the sequence's units in turn; their parts meet in LDS, and that is all.
 //   Else a wave takes a head tile and a piece of all sequences' units in a row. As many waves as
-//   run
-//   at once all take the same number of units, however the lengths differ; a wave may so end one
-//   sequence, take others whole and begin a last one. What it has of a sequence that was cut goes
-//   to
-//   memory, and a second kernel joins it. The waves of a workgroup have neighbouring heads of the
-//   same
-//   keys, which a cache laid out by tokens has side by side.
+//   run at once all take the same number of units, however the lengths differ; a wave may so end
+//   one sequence, take others whole and begin a last one. What it has of a sequence that was cut
+//   goes to memory, and a second kernel joins it. The waves of a workgroup have neighbouring heads
+//   of the same keys, which a cache laid out by tokens has side by side.
 struct DecodeArgs {
   fp8rl_attn_decode_args a;
   float* part;  // [wave][ended, begun][heads of a tile][head_dim], behind them their [m, l]
@@ -515,9 +527,9 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256) void attn_decode_join_kernel(
 namespace {
 
 // Pieces of all sequences' units, 0 where a workgroup takes a sequence.
-int decode_lots(int64_t heads, int64_t max_keys, int window) {
+int decode_lots(int64_t heads, int64_t max_keys, int window, int row_bytes) {
   if (window) max_keys = min(max_keys, (int64_t)window);
-  if (max_keys <= kWhole) return 0;
+  if (max_keys <= min(kWhole, kWholeBytes / row_bytes)) return 0;
   return (int)max((int64_t)1, 256 * kWaves / heads);
 }
 
@@ -546,7 +558,7 @@ size_t attn_decode_workspace(int64_t B, int q_heads, int kv_heads, int head_dim,
                              int window) {
   if (B == 0) return 0;
   const int64_t heads = (int64_t)kv_heads * head_tiles(q_heads, kv_heads);
-  return (size_t)(2 * heads * decode_lots(heads, max_keys, window)) *
+  return (size_t)(2 * heads * decode_lots(heads, max_keys, window, 2 * head_dim)) *
          (size_t)min(16, q_heads / kv_heads) * (size_t)(head_dim + 2) * sizeof(float);
 }
 
@@ -558,7 +570,8 @@ hipError_t launch_attn_decode(const fp8rl_attn_decode_args& a, void* workspace, 
   d.group = a.q_heads / a.kv_heads;
   d.tiles = head_tiles(a.q_heads, a.kv_heads);
   d.heads = a.kv_heads * d.tiles;
-  d.lots = decode_lots(d.heads, (int64_t)a.table_width * a.page_size, a.window);
+  d.lots = decode_lots(d.heads, (int64_t)a.table_width * a.page_size, a.window,
+                       a.head_dim * (a.k_scale ? 1 : 2));
   if (d.lots == 0) {
     a.k_scale ? run_decode<true, false>(d, stream) : run_decode<false, false>(d, stream);
     return hipGetLastError();

@@ -54,6 +54,10 @@ struct DocTile {
 // many tiles there are of at least k is a sum over the documents, one to a lane, and k is found by
 // its bits.
 //
+// (The gradients of six uneven documents of 4096 tokens in all: 202 us, document after document
+// 220; the output of four, 2048 queries behind 4096 keys, a window of 1024: 30.7 and 36.5. The
+// search takes about a microsecond.)
+//
 // More documents: from the last (with KEYS the first) document's on. Documents take
 //   rows[d + 1] / BM + d + 1 - (rows[d] / BM + d)  >=  ceil(length / BM)
 // places each, so that a tile is found from the offsets alone.

@@ -121,19 +121,21 @@ def test_decode_refusals(L):
 
 def test_decode_workspace(L):
     need = L.fp8rl_attn_decode_workspace_bytes
-    assert need(4, 8, 2, 128, 512, 0) == 0  # nothing is split up to there
+    assert need(4, 8, 2, 128, 1024, 0) == 0  # nothing is split up to there
+    assert need(4, 8, 2, 256, 512, 0) == 0  # nor up to 256 KiB of a head's keys
+    assert need(4, 8, 2, 256, 513, 0) > 0
     assert need(4, 8, 2, 128, 1 << 20, 200) == 0
-    big = need(4, 8, 2, 128, 513, 0)
+    big = need(4, 8, 2, 128, 1025, 0)
     assert big == 2 * 2048 * 4 * 130 * 4  # two rows of four heads for each of 2048 waves
     assert need(4, 8, 2, 128, 1 << 30, 0) == big  # bounded by the waves, not the length
     assert need(4, 8, 2, 128, 1 << 30, (1 << 31) - 1) == big
     assert need(0, 8, 2, 128, 1 << 30, 0) == 0
-    for bad in ((-1, 8, 2, 128, 513, 0), (4, 7, 2, 128, 513, 0), (4, 8, 2, 120, 513, 0),
-                (4, 8, 2, 128, -1, 0), (4, 8, 2, 128, (1 << 30) + 1, 0), (4, 8, 2, 128, 513, -1)):
+    for bad in ((-1, 8, 2, 128, 1025, 0), (4, 7, 2, 128, 1025, 0), (4, 8, 2, 120, 1025, 0),
+                (4, 8, 2, 128, -1, 0), (4, 8, 2, 128, (1 << 30) + 1, 0), (4, 8, 2, 128, 1025, -1)):
         assert need(*bad) == 0, bad
     args = _attn.AttnDecodeArgs(**dict(CACHE, q=A, ld_q=1024, B=4, q_heads=8, lengths=A, sm_scale=0.1,
-                                       out=A, ld_out=1024, table_width=64, ld_table=64))
-    n = need(4, 8, 2, 128, 1024, 0)
+                                       out=A, ld_out=1024, table_width=128, ld_table=128))
+    n = need(4, 8, 2, 128, 2048, 0)
     assert L.fp8rl_attn_decode(ctypes.byref(args), None, n, None) == EWS
     assert L.fp8rl_attn_decode(ctypes.byref(args), A, n - 1, None) == EWS
     assert L.fp8rl_attn_decode(ctypes.byref(args), A + 8, n, None) == EALIGN

@@ -40,16 +40,17 @@ def one(x):
 
 class Paged:
     """Caches of N(0, 1) rows for sequences of these lengths, pages in random order, NaN in every
-    place that no sequence has; table entries behind a sequence's last page are garbage."""
+    place that no sequence has; table entries behind a sequence's last page are garbage. The table
+    has room for `wide` keys at least (a call with a wide table splits short sequences too)."""
 
     def __init__(self, lens, Hkv, D, *, page=16, codes=True, heads_first=False, seed=0, spare=2,
-                 clean=0):
+                 wide=0):
         rng = np.random.default_rng(seed)
         self.lens, self.Hkv, self.D, self.page, self.codes = lens, Hkv, D, page, codes
         need = [-(-n // page) for n in lens]
         pages = sum(need) + spare
         order = rng.permutation(pages)
-        width = max(need + [1]) + 1
+        width = max(need + [1, -(-wide // page)]) + 1
         self.table = rng.integers(-5, 2 ** 31 - 1, (len(lens), width)).astype(np.int32)
         self.table[rng.random(self.table.shape) < 0.5] = -1
         shape = (pages, Hkv, page, D) if heads_first else (pages, page, Hkv, D)
@@ -180,6 +181,33 @@ def test_split_sequences(codes):
     check([9000], 4, 1, 64, codes=codes, seed=5)
     check([5000, 3, 0, 2049, 640, 12001], 4, 2, 64, codes=codes, seed=6)
     check([7001, 6000], 4, 2, 64, codes=codes, seed=8, window=2500)
+
+
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("D", [16, 48, 64, 80, 96, 128, 144, 192, 256])
+def test_split_head_widths(D, codes):
+    check([77, 300, 0, 64], 6, 2, D, codes=codes, q8=not codes, seed=D, wide=4096)
+
+
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("heads_first", [True, False])
+@pytest.mark.parametrize("page", [1, 3, 16, 24, 100, 1024])
+def test_split_pages(page, heads_first, codes):
+    check([250, 61, 400], 4, 2, 64, page=page, heads_first=heads_first, codes=codes, seed=page,
+          wide=2048)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (7, 1), (16, 1), (17, 1), (40, 2), (64, 4)])
+def test_split_groups(Hq, Hkv):
+    check([65, 300], Hq, Hkv, 64, codes=Hq % 2 == 0, seed=Hq, wide=2000)
+
+
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("room", [400, 511, 512, 800, 1023, 1024])
+def test_room_around_the_split(room, D, codes):
+    """Tables with room for about as many keys as are not split (one more than the longest has)."""
+    check([room, 5, room - 30], 2, 1, D, codes=codes, page=1, seed=room)
 
 
 def test_many_sequences():
