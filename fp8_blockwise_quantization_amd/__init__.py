@@ -7,8 +7,9 @@ of the FP8 backward pass (transposed weight copy, 128x1 token groups, row-scaled
 GEMMs with the activation quantization fused in (dense, and grouped with the codes read through
 the router's token indices), and the operators between the linears: residual addition with
 root-mean-square norm and 1x128 codes, the experts' sort, dispatch and combine, and the rotated
-append to a paged KV cache. Tensors live on the GPU; the functions only marshal arguments into
-the C ABI (include/fp8rl.h, include/fp8rl_block.h).
+append to a paged KV cache, and attention: of single tokens over that cache, the cache read back,
+and of packed documents with its gradients. Tensors live on the GPU; the functions only marshal
+arguments into the C ABI (include/fp8rl.h, include/fp8rl_block.h, include/fp8rl_attn.h).
 """
 
 from ._lib import (  # noqa: F401

@@ -18,7 +18,7 @@
 // than 2300.) Where there are few keys, a key tile's queries are dealt out in parts, whose sums a
 // third kernel adds.
 //
-// 8192 causal tokens, 32 query heads on 8 of 128: 755 us for dq, 1.09 PFLOP/s of its three
+// 8192 causal tokens, 32 query heads on 8 of 128: 770 us for dq, 1.07 PFLOP/s of its three
 // products, 1145 us for dk and dv, 0.96 of their four; 1.9 ms in all, 0.72 PFLOP/s of the five that
 // the gradients need. Memory: 2.1 GB read by the second pass, 1.9 TB/s.
 #include <limits.h>

@@ -21,7 +21,7 @@
 // 64 uneven sequences of up to 4096 keys of 8 heads of 128 in E4M3, 57.8 us without, 53.1 with),
 // keys do not (their rows are read 64 bytes at a time, and the other half of a line was gone by the
 // next step: 35 us instead of 32 for a window of 1024 keys of 256). Those 64 sequences are 246 MB:
-// 49 us for this kernel, 5.0 TB/s, and 6 for the join; 529 MB, eight uneven sequences of up to
+// 47 us for this kernel, 5.2 TB/s, and 6 for the join; 529 MB, eight uneven sequences of up to
 // 32768 keys of 4 heads of 128 in bf16: 88 us, 6.0 TB/s, and 6. What lies beside the bytes is the
 // launch and the chain of lengths, table and first keys, about 4 us. Two tiles of keys under way in
 // a wave (59.9 against 57.4 us: 16 waves' registers become 8's) and sixteen waves a CU with half a

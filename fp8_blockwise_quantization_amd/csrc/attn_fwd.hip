@@ -11,7 +11,7 @@
 //
 // Bound by the matrix cores and by what stands between their instructions: two waves on a SIMD, one
 // in its products while the other is in its exponentials. 8192 causal tokens, 32 query heads on 8
-// of 128: 540 us, 1.02 PFLOP/s, 48 % of the cycles in matrix instructions, no LDS bank conflicts; a
+// of 128: 550 us, 1.0 PFLOP/s, 48 % of the cycles in matrix instructions, no LDS bank conflicts; a
 // library product of 8192^3 reaches 1.29. Heads of 64: 0.83 PFLOP/s (half the products per
 // exponential), of 256: 0.78 (eight waves, all registers taken). Four tiles in LDS instead of two,
 // with eight waves, changed nothing: it is not the loads that a tile waits for.

@@ -20,6 +20,8 @@
  *   a = c - slopes[h] |p - j|,     c = cap tanh(s / cap)   (s itself with cap == 0),
  * without the slopes' term where slopes is NULL, and out = sum_j softmax(a)_j v_j. A query that
  * sees no key gives zeros.
+ *
+ * Outputs and workspaces overlap no input and not one another; outputs may be columns of one row.
  */
 #ifndef FP8RL_ATTN_H
 #define FP8RL_ATTN_H
@@ -178,7 +180,6 @@ fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream);
  * result is rounded once. Deterministic: no atomics. Values of q, k, v and dout that are NaN or
  * infinite reach any row of their document, and no other document.
  *   workspace : at least fp8rl_attn_bwd_workspace_bytes(...) bytes, 16-byte aligned, overwritten
- * dq, dk and dv must not overlap the inputs or each other (columns of one fused row are fine).
  * Requires what fp8rl_attn_fwd does, and head_dim <= 128. Tq == Tk == 0 or docs == 0 returns FP8RL_OK.
  */
 fp8rl_status fp8rl_attn_bwd(const fp8rl_attn_args* args, void* workspace, size_t workspace_bytes,
