@@ -35,7 +35,13 @@ constexpr int kWaves = 4;
 constexpr int kOwn = 128;   // rows of a workgroup
 constexpr int kPass = 64;   // keys of a tile that the first pass goes through
 constexpr int kQueries = 64; // queries of a tile that the second goes through
-constexpr int kMostParts = 8;
+constexpr int kMostParts = 16;
+// Workgroups up to which, and keys of a document (on the average) from which on, two waves share 32
+// queries in the first pass: a tile takes less time with all of a CU's waves on it. All three
+// kernels, one document of 4096 tokens, 8 heads on 1 of 128: 235 us, else 270; 3000 tokens, 8 on 8:
+// 146, 170; 1024, 32 on 8: 86, 92. Documents of 128 on the average, 1024 in all: 68, else 60; one
+// of 256: 34.1, 33.2. 576 workgroups, two documents of 2048 in all, 32 on 4: 170, 167.
+constexpr int kFewQueries = 512, kLong = 512;
 
 // The tiles of queries that see any of a workgroup's keys, those of the group's heads one after
 // another.
@@ -86,14 +92,17 @@ __device__ __forceinline__ f32x4* part_of(const AttnArgs& d, int tile, int part,
 
 }  // namespace
 
-template <int DP, bool PAD, bool MORE>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
+// KH: waves that share 32 queries, each with its part of a tile's keys; their sums meet in the end.
+template <int DP, bool PAD, bool MORE, int KH>
+__global__ __launch_bounds__(256 * KH, 2) void attn_dq_kernel(AttnArgs d) {
   constexpr int KS = DP / 16, DT = DP / 32;
-  __shared__ __align__(1024) uint8_t s_k[2][kPass * DP * 2];
-  __shared__ __align__(1024) uint8_t s_v[2][kPass * DP * 2];
+  constexpr int kAll = 4 * KH, NR = 2 / KH;  // waves, a wave's 32-key parts of a tile
+  constexpr int kTile = kPass * DP * 2;      // bytes
+  __shared__ __align__(1024) uint8_t s_mem[4 * kTile];  // k and v of two tiles; then some waves' sums
   const fp8rl_attn_args& a = d.a;
   const int lane = (int)(threadIdx.x & 63), h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int block = wave & 3, part = wave >> 2;  // of the queries, of a tile's keys
   const int D = PAD ? a.head_dim : DP;
 
   const int id = (int)blockIdx.x;  // (the order is the forward pass's)
@@ -103,10 +112,10 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
   if (t.doc >= (int)a.docs) return;
   const Mask mask(a, t);
   const int shift = t.lk - t.lq;
-  const int row = t.first + 32 * wave + (lane & 31);
+  const int row = t.first + 32 * block + (lane & 31);
   const int p = row + shift;
-  const int rows = min(32, t.lq - t.first - 32 * wave);
-  const int p0 = t.first + 32 * wave + shift, p1 = p0 + rows - 1;
+  const int rows = min(32, t.lq - t.first - 32 * block);
+  const int p0 = t.first + 32 * block + shift, p1 = p0 + rows - 1;
   const bool in = row < t.lq;
   const int64_t qrow = t.q0 + min(row, t.lq - 1);
 
@@ -116,13 +125,13 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
   const int tiles = in_prefix + max(0, (mask.hi(last) + kPass - 1) / kPass - begin);
   auto key_of = [&](int i) { return kPass * (i < in_prefix ? i : i - in_prefix + begin); };
 
-  const RowLoader<DP, kPass, kWaves> rows_in(D, wave, lane);
+  const RowLoader<DP, kPass, kAll> rows_in(D, wave, lane);
   const uint16_t* const k0 = a.k + t.k0 * a.ld_k + (int64_t)kv * D;
   const uint16_t* const v0 = a.v + t.k0 * a.ld_v + (int64_t)kv * D;
   auto load = [&](int i) {
     const int j = key_of(i);
-    rows_in.load(k0 + j * a.ld_k, a.ld_k, t.lk - j, s_k[i & 1], wave);
-    rows_in.load(v0 + j * a.ld_v, a.ld_v, t.lk - j, s_v[i & 1], wave);
+    rows_in.load(k0 + j * a.ld_k, a.ld_k, t.lk - j, s_mem + 2 * (i & 1) * kTile, wave);
+    rows_in.load(v0 + j * a.ld_v, a.ld_v, t.lk - j, s_mem + (2 * (i & 1) + 1) * kTile, wave);
   };
   if (tiles > 0) load(0);
 
@@ -149,7 +158,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
   // a query that sees nothing: exp(S - inf) = 0 throughout
   float lse2 = a.lse[head * a.Tq + qrow] * kLog2e;
   if (lse2 == -__builtin_inff()) lse2 = __builtin_inff();
-  if (in && h == 0) {
+  if (in && h == 0 && part == 0) {
     d.stats[head * a.Tq + qrow] = lse2;
     d.stats[(a.q_heads + head) * a.Tq + qrow] = delta;
   }
@@ -164,15 +173,19 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
   for (int i = 0; i < tiles; ++i) {
     landed();
     if (i + 1 < tiles) load(i + 1);
-    const int j0 = key_of(i), keys = min(kPass, t.lk - j0);
-    if (keys < kPass) {
-      clear_rows<DP, kPass, kWaves>(s_k[i & 1], keys);
+    uint8_t *const s_k = s_mem + 2 * (i & 1) * kTile, *const s_v = s_k + kTile;
+    const int tile = key_of(i), in_tile = min(kPass, t.lk - tile);
+    if (in_tile < kPass) {
+      clear_rows<DP, kPass, kAll>(s_k, in_tile);
       __syncthreads();
     }
-    if (rows <= 0 || !mask.any(p0, p1, j0, j0 + keys)) continue;
+    // this wave's keys
+    constexpr int kMine = 32 * NR;
+    const int j0 = tile + kMine * part, keys = min(kMine, t.lk - j0);
+    if (rows <= 0 || keys <= 0 || !mask.any(p0, p1, j0, j0 + keys)) continue;
     const int lo = mask.lo(p), hi = mask.hi(p);
-    const RowOperand<DP> kop(s_k[i & 1], lane), vop(s_v[i & 1], lane);
-    const ColOperand<DP> kt(s_k[i & 1], lane);
+    const RowOperand<DP> kop(s_k + kMine * part * DP * 2, lane), vop(s_v + kMine * part * DP * 2, lane);
+    const ColOperand<DP> kt(s_k + kMine * part * DP * 2, lane);
     f32x16 s, dp;
     auto weigh = [&](int r, auto masked) {  // dS in its place
       if (MORE) {
@@ -190,9 +203,9 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
         s[e] = !masked || (j < mask.prefix) | ((j >= lo) & (j < hi)) ? ds : 0.f;
       }
     };
-    const bool all = keys == kPass && mask.all(p0, p1, j0, j0 + kPass);
+    const bool all = keys == kMine && mask.all(p0, p1, j0, j0 + kMine);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {  // 32 keys
+    for (int r = 0; r < NR; ++r) {  // 32 keys
       s = zeros16(), dp = zeros16();
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
@@ -213,6 +226,25 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs d) {
           o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt(32 * r + 16 * u, c), w, o[c], 0, 0, 0);
         }
       }
+    }
+  }
+  if (KH > 1) {
+    landed();
+    f32x4* const other = reinterpret_cast<f32x4*>(s_mem) + block * (64 * 4 * DT) + lane;
+    if (part == 1) {
+#pragma unroll
+      for (int c = 0; c < 4 * DT; ++c) {
+        const int e = 4 * (c & 3);
+        other[64 * c] = f32x4{o[c >> 2][e], o[c >> 2][e + 1], o[c >> 2][e + 2], o[c >> 2][e + 3]};
+      }
+    }
+    __syncthreads();
+    if (part == 1) return;
+#pragma unroll
+    for (int c = 0; c < 4 * DT; ++c) {
+      const f32x4 x = other[64 * c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c >> 2][4 * (c & 3) + e] += x[e];
     }
   }
   if (rows <= 0) return;
@@ -423,23 +455,30 @@ __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs d) {
   const int lane = (int)(threadIdx.x & 63);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int kv = (int)blockIdx.x % a.kv_heads, c = (int)blockIdx.y;
-  f32x4 x[kMostParts][4];
+  constexpr int kFlight = 8;  // parts whose loads are under way at a time
+  f32x4 x[kFlight][4];
+  auto load = [&](int first) {
 #pragma unroll
-  for (int part = 0; part < kMostParts; ++part) {
-    if (part >= d.parts) break;
-    const f32x4* const from = part_of<DP>(d, (int)blockIdx.x, part, wave, lane) + 64 * 4 * c;
+    for (int i = 0; i < kFlight; ++i) {
+      if (first + i >= d.parts) break;
+      const f32x4* const from = part_of<DP>(d, (int)blockIdx.x, first + i, wave, lane) + 64 * 4 * c;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[part][e] = from[64 * e];
-  }
+      for (int e = 0; e < 4; ++e) x[i][e] = from[64 * e];
+    }
+  };
+  load(0);
   const DocTile t = find_tile<kOwn, true>(d, (int)blockIdx.x / a.kv_heads, lane);
   const int key = t.first + 32 * wave;
   if (t.doc >= (int)a.docs || key >= t.lk) return;
   f32x16 g = zeros16();
+  for (int first = 0; first < d.parts; first += kFlight) {
+    if (first > 0) load(first);
 #pragma unroll
-  for (int part = 0; part < kMostParts; ++part) {
-    if (part >= d.parts) break;
+    for (int i = 0; i < kFlight; ++i) {
+      if (first + i >= d.parts) break;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) g[e] += x[part][e >> 2][e & 3];
+      for (int e = 0; e < 16; ++e) g[e] += x[i][e >> 2][e & 3];
+    }
   }
   const int64_t row = t.k0 + key + (lane & 31);
   uint16_t* const to = c < DT ? a.dk + row * a.ld_dk : a.dv + row * a.ld_dv;
@@ -449,13 +488,18 @@ __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs d) {
 
 namespace {
 
-// Parts that a key tile's queries are dealt out in, for two and a half workgroups to a CU. (What
-// splitting costs is the parts' way through memory, 8 bytes a value of dk and dv and part, each
-// way. The gradients of six documents of 4096 tokens in all, 32 query heads on 4 of 128: 202 us;
-// with 512 for 640 217, with 768 209, with 1024 215.)
-int key_parts(int64_t Tk, int64_t docs, int kv_heads) {
-  const int64_t tiles = (Tk / kOwn + docs) * kv_heads;
-  return (int)max((int64_t)1, min((int64_t)kMostParts, 640 / max((int64_t)1, tiles)));
+// Parts that a key tile's queries are dealt out in: up to eight for two and a half workgroups to a
+// CU, and more for two to a CU where eight tiles of queries a part remain. (What splitting costs is
+// the parts' way through memory, 8 bytes a value of dk and dv and part, each way. The gradients of
+// six documents of 4096 tokens in all, 32 query heads on 4 of 128: 202 us; with 512 workgroups for
+// 640 217, with 768 209, with 1024 215. One document, 8 heads on 1, with sixteen and with eight
+// parts: 4096 tokens 192 and 235 us, 2048 101 and 128; 8192, nine parts for eight, 603 and 580;
+// 512, 32 on 8, two tiles a part, 62 and 49.)
+int key_parts(int64_t Tq, int64_t Tk, int64_t docs, int q_heads, int kv_heads) {
+  const int64_t tiles = max((int64_t)1, (Tk / kOwn + docs) * kv_heads);
+  const int64_t through = Tq / kQueries * (q_heads / kv_heads) / max((int64_t)1, docs);
+  const int64_t more = min((int64_t)kMostParts, min(through / 8, 528 / tiles));
+  return (int)max(max((int64_t)1, more), min((int64_t)8, 640 / tiles));
 }
 
 int padded(int head_dim) { return head_dim <= 64 ? 64 : 128; }
@@ -464,7 +508,7 @@ int padded(int head_dim) { return head_dim <= 64 ? 64 : 128; }
 
 size_t attn_bwd_workspace(int64_t Tq, int64_t Tk, int64_t docs, int q_heads, int kv_heads,
                           int head_dim) {
-  const int64_t parts = key_parts(Tk, docs, kv_heads);
+  const int64_t parts = key_parts(Tq, Tk, docs, q_heads, kv_heads);
   const int64_t stats = (2 * Tq * q_heads + 3) / 4 * 4;
   const int64_t part = parts > 1 ? (Tk / kOwn + docs) * kv_heads * parts * kOwn * 2 : 0;
   return (size_t)(stats + part * padded(head_dim)) * sizeof(float);
@@ -473,28 +517,38 @@ size_t attn_bwd_workspace(int64_t Tq, int64_t Tk, int64_t docs, int q_heads, int
 hipError_t launch_attn_bwd(const fp8rl_attn_args& a, float* workspace, hipStream_t stream) {
   AttnArgs q = attn_args(a, kOwn, a.Tq), k = attn_args(a, kOwn, a.Tk);
   q.stats = k.stats = workspace;
-  k.parts = key_parts(a.Tk, a.docs, a.kv_heads);
+  k.parts = key_parts(a.Tq, a.Tk, a.docs, a.q_heads, a.kv_heads);
   k.part = workspace + (2 * a.Tq * a.q_heads + 3) / 4 * 4;
   const dim3 block(64 * kWaves);
   const dim3 grid_q((unsigned)(q.slots * a.q_heads)), grid_k((unsigned)(k.slots * a.kv_heads * k.parts)),
       grid_j((unsigned)(k.slots * a.kv_heads), (unsigned)(2 * padded(a.head_dim) / 32));
-  auto go = [&](auto dq, auto dkv) {
-    hipLaunchKernelGGL(dq, grid_q, block, 0, stream, q);
+  const bool few = q.slots * a.q_heads <= kFewQueries && a.Tk >= kLong * a.docs;
+  auto go = [&](auto one, auto two, auto dkv) {
+    if (few)
+      hipLaunchKernelGGL(two, grid_q, dim3(512), 0, stream, q);
+    else
+      hipLaunchKernelGGL(one, grid_q, block, 0, stream, q);
     hipLaunchKernelGGL(dkv, grid_k, dim3(512), 0, stream, k);
   };
-  const bool more = a.cap > 0.f || a.slopes;
+  auto choose = [&](auto width, auto pad) {
+    constexpr int DP = decltype(width)::value;
+    constexpr bool PAD = decltype(pad)::value;
+    a.cap > 0.f || a.slopes
+        ? go(attn_dq_kernel<DP, PAD, true, 1>, attn_dq_kernel<DP, PAD, true, 2>,
+             attn_dkv_kernel<DP, PAD, true>)
+        : go(attn_dq_kernel<DP, PAD, false, 1>, attn_dq_kernel<DP, PAD, false, 2>,
+             attn_dkv_kernel<DP, PAD, false>);
+  };
+  constexpr std::integral_constant<int, 64> k64;
+  constexpr std::integral_constant<int, 128> k128;
   if (a.head_dim == 64)
-    more ? go(attn_dq_kernel<64, false, true>, attn_dkv_kernel<64, false, true>)
-         : go(attn_dq_kernel<64, false, false>, attn_dkv_kernel<64, false, false>);
+    choose(k64, std::false_type{});
   else if (a.head_dim < 64)
-    more ? go(attn_dq_kernel<64, true, true>, attn_dkv_kernel<64, true, true>)
-         : go(attn_dq_kernel<64, true, false>, attn_dkv_kernel<64, true, false>);
+    choose(k64, std::true_type{});
   else if (a.head_dim < 128)
-    more ? go(attn_dq_kernel<128, true, true>, attn_dkv_kernel<128, true, true>)
-         : go(attn_dq_kernel<128, true, false>, attn_dkv_kernel<128, true, false>);
+    choose(k128, std::true_type{});
   else
-    more ? go(attn_dq_kernel<128, false, true>, attn_dkv_kernel<128, false, true>)
-         : go(attn_dq_kernel<128, false, false>, attn_dkv_kernel<128, false, false>);
+    choose(k128, std::false_type{});
   if (k.parts > 1) {
     if (padded(a.head_dim) == 64)
       hipLaunchKernelGGL(attn_dkv_join_kernel<64>, grid_j, block, 0, stream, k);

@@ -231,6 +231,27 @@ def test_long_window_and_prefix_far_apart():
     check_bwd(d)
 
 
+@pytest.mark.parametrize("D", [64, 80, 128])
+@pytest.mark.parametrize("more", [{}, dict(causal=False), dict(window=300, prefix=[5, 80]),
+                                  dict(cap=20.0, slopes=True, window=200)])
+def test_long_documents_of_few_heads(more, D):
+    """Two waves to a query in both directions, and a key's queries in more than eight parts."""
+    d = Docs([700, 530], D=D, Hq=8, Hkv=1, seed=13, **more)
+    check_fwd(d)
+    check_bwd(d)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("more", MASKS)
+def test_masks_with_many_workgroups(more, D):
+    """As in long calls: one wave to a query."""
+    if "prefix" in more:
+        more = dict(more, prefix=more["prefix"] + [0] * 40)
+    d = Docs([65, 140, 300] + [0] * 40, D=D, Hq=16, Hkv=4, seed=5, **more)
+    check_fwd(d)
+    check_bwd(d)
+
+
 def test_many_documents():
     rng = np.random.default_rng(0)
     lens = rng.integers(0, 4, 400).tolist()
