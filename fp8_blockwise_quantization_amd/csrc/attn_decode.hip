@@ -49,11 +49,14 @@ constexpr int kLeast = 2;   // units of a piece
 //   Else a wave takes a head tile and a piece of all sequences' units in a row. As many waves as
 //   run at once all take the same number of units, however the lengths differ; a wave may so end
 //   one sequence, take others whole and begin a last one. What it has of a sequence that was cut
-//   goes to memory, and a second kernel joins it. The waves of a workgroup have neighbouring heads
+//   goes to memory, and a second kernel joins it, told by the wave that began it where it lies
+//   (counted anew for each head, 4096 sequences of 160 keys took 286 us instead of 145). The waves
+//   of a workgroup have neighbouring heads
 //   of the same keys, which a cache laid out by tokens has side by side.
 struct DecodeArgs {
   fp8rl_attn_decode_args a;
   float* part;  // [wave][ended, begun][heads of a tile][head_dim], behind them their [m, l]
+  int* cut;     // behind those [B]: the units in front of a sequence, -1 if it is whole; [1]: a lot's
   PageOf page_of;
   int group;   // query heads of a key head
   int tiles;   // of 16 query heads of a key head
@@ -82,8 +85,8 @@ struct Place {
   int per;
 };
 
-// Of the sequence that holds unit per * lot (b = B: none does), or of sequence `b`.
-__device__ __forceinline__ Place find_place(const DecodeArgs& d, int lot, int b, int lane) {
+// Of the sequence that holds unit per * lot (b = B: none does).
+__device__ __forceinline__ Place find_place(const DecodeArgs& d, int lot, int lane) {
   const int B = (int)d.a.B;
   const int front = sum_upto(keys_of(d, lane).units);  // most calls' only sequences
   int total = __builtin_amdgcn_readlane(front, 63);
@@ -93,7 +96,7 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& d, int lot, int b,
   int base = 0;
   for (int c = 0; c < B; c += 64) {
     const int upto = base + (c == 0 ? front : sum_upto(keys_of(d, c + lane).units));
-    const uint64_t here = __ballot(c + lane < B && (lot >= 0 ? upto > lot * per : c + lane == b));
+    const uint64_t here = __ballot(c + lane < B && upto > lot * per);
     if (here) {
       const int at = __builtin_ctzll(here);
       return {c + at, at ? __builtin_amdgcn_readlane(upto, at - 1) : base, per};
@@ -219,6 +222,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
         before += keys.units;
         if (to == 0) continue;  // (a sequence without keys is left to the join)
         begun = from == 0, whole = begun && to == keys.units;
+        if (begun && head == 0 && lane == 0) d.cut[b] = whole ? -1 : taken;
         taken += to - from;
         end = min(keys.last, (keys.unit + to) * kUnit);
         base = (keys.unit + from) * kUnit;
@@ -256,8 +260,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs 
 
   b = lot;
   if (SPLIT) {
-    const Place p = find_place(d, lot, 0, lane);
+    const Place p = find_place(d, lot, lane);
     b = p.b, before = p.before, taken = lot * p.per, stop = taken + p.per;
+    if (id == 0 && lane == 0) d.cut[a.B] = p.per;
   }
   bool more = next();
   if (more) start();
@@ -466,7 +471,6 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256) void attn_decode_join_kernel(
   const int x = (int)blockIdx.x * kItems + wave / W, part = wave % W;
   const int b = x / a.q_heads, hq = x - b * a.q_heads;
   if (b >= (int)a.B) return;
-  const Place place = find_place(d, -1, b, lane);
   const Keys keys = keys_of(d, b);
   const bool has = 4 * lane < a.head_dim;
   u32x2* const out =
@@ -475,9 +479,9 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256) void attn_decode_join_kernel(
     if (has && part == 0) out[lane] = u32x2{0u, 0u};
     return;
   }
-  const int lot = place.before / place.per;
-  const int pieces = (place.before + keys.units - 1) / place.per - lot + 1;
-  if (pieces == 1) return;
+  const int before = d.cut[b], per = d.cut[a.B];
+  if (before < 0) return;
+  const int lot = before / per, pieces = (before + keys.units - 1) / per - lot + 1;
   const int kv = hq / d.group, in = hq - kv * d.group;
   const int most = min(16, d.group);
   // the row that piece i left: the first began the sequence, the others end it or go on
@@ -550,6 +554,11 @@ void run_decode(const DecodeArgs& d, hipStream_t stream) {
              : go(attn_decode_kernel<256, true, CODES, SPLIT>);
 }
 
+// Of all parts, with their statistics.
+int64_t part_floats(int64_t waves, int group, int head_dim) {
+  return 2 * waves * min(16, group) * (head_dim + 2);
+}
+
 int head_tiles(int q_heads, int kv_heads) { return (q_heads / kv_heads + 15) / 16; }
 
 }  // namespace
@@ -558,8 +567,10 @@ size_t attn_decode_workspace(int64_t B, int q_heads, int kv_heads, int head_dim,
                              int window) {
   if (B == 0) return 0;
   const int64_t heads = (int64_t)kv_heads * head_tiles(q_heads, kv_heads);
-  return (size_t)(2 * heads * decode_lots(heads, max_keys, window, 2 * head_dim)) *
-         (size_t)min(16, q_heads / kv_heads) * (size_t)(head_dim + 2) * sizeof(float);
+  const int64_t lots = decode_lots(heads, max_keys, window, 2 * head_dim);
+  if (lots == 0) return 0;
+  return (size_t)part_floats(heads * lots, q_heads / kv_heads, head_dim) * sizeof(float) +
+         (size_t)(B + 1) * sizeof(int);
 }
 
 hipError_t launch_attn_decode(const fp8rl_attn_decode_args& a, void* workspace, hipStream_t stream) {
@@ -576,6 +587,7 @@ hipError_t launch_attn_decode(const fp8rl_attn_decode_args& a, void* workspace, 
     a.k_scale ? run_decode<true, false>(d, stream) : run_decode<false, false>(d, stream);
     return hipGetLastError();
   }
+  d.cut = reinterpret_cast<int*>(d.part + part_floats((int64_t)d.heads * d.lots, d.group, a.head_dim));
   a.k_scale ? run_decode<true, true>(d, stream) : run_decode<false, true>(d, stream);
   // a wave has sixteen of a sequence's parts in flight at a time; where there are more, eight waves
   // share them

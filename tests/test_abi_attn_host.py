@@ -126,7 +126,8 @@ def test_decode_workspace(L):
     assert need(4, 8, 2, 256, 513, 0) > 0
     assert need(4, 8, 2, 128, 1 << 20, 200) == 0
     big = need(4, 8, 2, 128, 1025, 0)
-    assert big == 2 * 2048 * 4 * 130 * 4  # two rows of four heads for each of 2048 waves
+    # two rows of four heads for each of 2048 waves, a word of every sequence and one of all
+    assert big == 2 * 2048 * 4 * 130 * 4 + 5 * 4
     assert need(4, 8, 2, 128, 1 << 30, 0) == big  # bounded by the waves, not the length
     assert need(4, 8, 2, 128, 1 << 30, (1 << 31) - 1) == big
     assert need(0, 8, 2, 128, 1 << 30, 0) == 0

@@ -216,6 +216,12 @@ def test_many_sequences():
     check(rng.integers(0, 1500, 70).tolist(), 2, 2, 16, codes=False, seed=10)
 
 
+def test_many_sequences_of_a_wide_table():
+    rng = np.random.default_rng(3)
+    check(rng.integers(0, 90, 300).tolist(), 4, 2, 32, codes=True, seed=9, wide=2000)
+    check([0] * 130 + [400] + [0] * 80 + [65, 1], 2, 1, 16, codes=False, seed=9, wide=2000)
+
+
 def test_bad_pages_are_not_seen():
     paged = Paged([600, 40], 2, 64, seed=3)
     paged.table[0, 3] = -1
