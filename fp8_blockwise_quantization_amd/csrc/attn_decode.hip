@@ -51,12 +51,12 @@ constexpr int kLeast = 2;   // units of a piece
 //   one sequence, take others whole and begin a last one. What it has of a sequence that was cut
 //   goes to memory, and a second kernel joins it, told by the wave that began it where it lies
 //   (counted anew for each head, 4096 sequences of 160 keys took 286 us instead of 145). The waves
-//   of a workgroup have neighbouring heads
-//   of the same keys, which a cache laid out by tokens has side by side.
+//   of a workgroup have neighbouring heads of the same keys, which a cache laid out by tokens has
+//   side by side.
 struct DecodeArgs {
   fp8rl_attn_decode_args a;
   float* part;  // [wave][ended, begun][heads of a tile][head_dim], behind them their [m, l]
-  int* cut;     // behind those [B]: the units in front of a sequence, -1 if it is whole; [1]: a lot's
+  int* cut;     // behind those [B]: units in front of a sequence, -1 if it is whole; [1]: of a lot
   PageOf page_of;
   int group;   // query heads of a key head
   int tiles;   // of 16 query heads of a key head
