@@ -34,7 +34,6 @@ hipError_t launch_kv_read(const fp8rl_kv_read_args& a, hipStream_t stream);
 constexpr float kLog2e = 1.4426950408889634f;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -98,14 +97,10 @@ __device__ __forceinline__ float sum_rows(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// Four E4M3 codes as two words of bf16 or of fp16 pairs (exact).
+// Four E4M3 codes as two words of bf16 pairs (exact).
 __device__ __forceinline__ u32x2 codes_bf16(uint32_t w) {
   return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false)),
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true))};
-}
-__device__ __forceinline__ u32x2 codes_f16(uint32_t w) {
-  return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false)),
-               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true))};
 }
 
 // The page that holds a key: key / page_size by a product with ceil(2^62 / page_size), exact for

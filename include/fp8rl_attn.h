@@ -67,9 +67,8 @@ typedef struct {
  * A length counts as at most table_width * page_size, and as 0 where it is negative. A key whose
  * page lies outside [0, num_pages) is not seen. What the cache holds in places that are not seen
  * (behind a sequence's end, before its window) is of no consequence, NaN and infinities included.
- * Sums and statistics are float32. The weights are rounded to fp16 for the products with an E4M3
- * cache's values; for a bf16 cache's they are split in two bf16 terms (16 bits). out is rounded
- * once. Deterministic; where sequences are split over waves, the cuts follow from all the lengths
+ * Sums and statistics are float32. For their products with the values the weights are split in two
+ * bf16 terms (16 bits, however small a weight is beside the largest). out is rounded once. Deterministic; where sequences are split over waves, the cuts follow from all the lengths
  * of the call, so that a sequence's last bits can change with its neighbours.
  *   workspace : at least fp8rl_attn_decode_workspace_bytes(...) bytes, 16-byte aligned,
  *               overwritten; may be NULL when that is 0
