@@ -162,7 +162,9 @@ fp8rl_status fp8rl_kv_read(const fp8rl_kv_read_args* args, void* stream) {
 
 namespace {
 
-constexpr int64_t kMaxPitch = int64_t{1} << 24;  // 64 rows are less than 2^32 bytes apart
+constexpr int64_t kMaxPitch = int64_t{1} << 24;  // 128 rows are less than 2^32 bytes apart
+// A dispatch has fewer than 2^32 threads: so many workgroups of 256, and of 512, are past it.
+constexpr int64_t kMax256 = int64_t{1} << 24, kMax512 = int64_t{1} << 23;
 
 fp8rl_status check_attn_sizes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_heads,
                               int32_t kv_heads, int32_t head_dim, int32_t widest) {
@@ -170,14 +172,18 @@ fp8rl_status check_attn_sizes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_he
   if (Tq < 0 || Tk < 0 || Tq >= kRows || Tk >= kRows) return FP8RL_ERR_SHAPE;
   if (docs < 0 || docs >= (int64_t{1} << 20)) return FP8RL_ERR_SHAPE;
   if (fp8rl_status s = check_heads(q_heads, kv_heads, head_dim, widest)) return s;
-  if (((Tq > Tk ? Tq : Tk) / 128 + docs) * q_heads >= (int64_t{1} << 24)) return FP8RL_ERR_SHAPE;
+  if (((Tq > Tk ? Tq : Tk) / 128 + docs) * q_heads >= kMax256) return FP8RL_ERR_SHAPE;
   return FP8RL_OK;
 }
 
-fp8rl_status check_attn_shape(const fp8rl_attn_args& a, int32_t widest) {
-  if (fp8rl_status s =
-          check_attn_sizes(a.Tq, a.Tk, a.docs, a.q_heads, a.kv_heads, a.head_dim, widest))
-    return s;
+fp8rl_status check_bwd_sizes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_heads,
+                             int32_t kv_heads, int32_t head_dim) {
+  if (fp8rl_status s = check_attn_sizes(Tq, Tk, docs, q_heads, kv_heads, head_dim, 128)) return s;
+  // (dk's and dv's workgroups have 512 threads)
+  return (Tk / 128 + docs) * kv_heads < kMax512 ? FP8RL_OK : FP8RL_ERR_SHAPE;
+}
+
+fp8rl_status check_attn_scores(const fp8rl_attn_args& a) {
   if (a.causal != 0 && a.causal != 1) return FP8RL_ERR_ARG;
   if (fp8rl_status s = check_scores(a.sm_scale, a.window, a.cap)) return s;
   return a.sm_scale > 0.f ? FP8RL_OK : FP8RL_ERR_ARG;
@@ -209,7 +215,12 @@ fp8rl_status check_attn_inputs(const fp8rl_attn_args& a) {
 fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream) {
   if (!args) return FP8RL_ERR_NULL;
   const fp8rl_attn_args& a = *args;
-  if (fp8rl_status s = check_attn_shape(a, 256)) return s;
+  if (fp8rl_status s =
+          check_attn_sizes(a.Tq, a.Tk, a.docs, a.q_heads, a.kv_heads, a.head_dim, 256))
+    return s;
+  // (heads past 128 columns: workgroups of 512 threads)
+  if (a.head_dim > 128 && (a.Tq / 128 + a.docs) * a.q_heads >= kMax512) return FP8RL_ERR_SHAPE;
+  if (fp8rl_status s = check_attn_scores(a)) return s;
   if (a.Tq == 0 || a.docs == 0) return FP8RL_OK;
   if (fp8rl_status s = check_attn_inputs(a)) return s;
   return hip_status(fp8rl::launch_attn_fwd(a, as_stream(stream)));
@@ -217,7 +228,7 @@ fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream) {
 
 size_t fp8rl_attn_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int64_t docs, int32_t q_heads,
                                       int32_t kv_heads, int32_t head_dim) {
-  if (check_attn_sizes(Tq, Tk, docs, q_heads, kv_heads, head_dim, 128) != FP8RL_OK) return 0;
+  if (check_bwd_sizes(Tq, Tk, docs, q_heads, kv_heads, head_dim) != FP8RL_OK) return 0;
   return fp8rl::attn_bwd_workspace(Tq, Tk, docs, q_heads, kv_heads, head_dim);
 }
 
@@ -225,7 +236,9 @@ fp8rl_status fp8rl_attn_bwd(const fp8rl_attn_args* args, void* workspace, size_t
                             void* stream) {
   if (!args) return FP8RL_ERR_NULL;
   const fp8rl_attn_args& a = *args;
-  if (fp8rl_status s = check_attn_shape(a, 128)) return s;
+  if (fp8rl_status s = check_bwd_sizes(a.Tq, a.Tk, a.docs, a.q_heads, a.kv_heads, a.head_dim))
+    return s;
+  if (fp8rl_status s = check_attn_scores(a)) return s;
   if ((a.Tq == 0 && a.Tk == 0) || a.docs == 0) return FP8RL_OK;
   const int64_t qc = (int64_t)a.q_heads * a.head_dim, kc = (int64_t)a.kv_heads * a.head_dim;
   if (!a.q_offsets || !a.k_offsets) return FP8RL_ERR_NULL;

@@ -162,7 +162,7 @@ typedef struct {
  * 0 * NaN does); they reach no other document.
  * Requires head_dim % 16 == 0, 16 <= head_dim <= 256, 1 <= kv_heads, q_heads a multiple of
  * kv_heads, q_heads <= 4096, Tq, Tk < 2^24, docs < 2^20,
- * (max(Tq, Tk) / 128 + docs) * q_heads < 2^24,
+ * (max(Tq, Tk) / 128 + docs) * q_heads < 2^24, past 128 columns (Tq / 128 + docs) * q_heads < 2^23,
  * 0 < sm_scale <= 2^60, window >= 0, cap 0 or within 2^-60 .. 2^60; 16-byte aligned rows, pitches
  * multiples of 8, >= the columns and < 2^24; offsets, prefix, lse and slopes 4-byte aligned.
  * Tq == 0 or docs == 0 returns FP8RL_OK.
@@ -179,7 +179,8 @@ fp8rl_status fp8rl_attn_fwd(const fp8rl_attn_args* args, void* stream);
  * result is rounded once. Deterministic: no atomics. Values of q, k, v and dout that are NaN or
  * infinite reach any row of their document, and no other document.
  *   workspace : at least fp8rl_attn_bwd_workspace_bytes(...) bytes, 16-byte aligned, overwritten
- * Requires what fp8rl_attn_fwd does, and head_dim <= 128. Tq == Tk == 0 or docs == 0 returns FP8RL_OK.
+ * Requires what fp8rl_attn_fwd does, head_dim <= 128 and (Tk / 128 + docs) * kv_heads < 2^23. Tq == Tk
+ * == 0 or docs == 0 returns FP8RL_OK.
  */
 fp8rl_status fp8rl_attn_bwd(const fp8rl_attn_args* args, void* workspace, size_t workspace_bytes,
                             void* stream);

@@ -4,9 +4,12 @@ are those of the tests whose helpers these are."""
 
 import numpy as np
 import pytest
+import torch
 
-from tests.test_gpu_attn_decode import check
-from tests.test_gpu_attn_docs import Docs, check_bwd, check_fwd
+import fp8_blockwise_quantization_amd as fq
+from tests.gpu_util import assert_within
+from tests.test_gpu_attn_decode import check, f64
+from tests.test_gpu_attn_docs import Docs, check_bwd, check_fwd, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +66,34 @@ def test_a_long_sequence_among_many(Hkv, short, long, codes):
     per = max(2, -(-units.sum() // lots))
     assert lots <= 16 * len(lens) and -(-long // 32) / per > 17
     check(lens, 2 * Hkv, Hkv, 64, codes=codes, seed=Hkv)
+
+
+@pytest.mark.parametrize("D", [16, 144])
+def test_as_many_workgroups_as_a_launch_takes(D):
+    """Documents of a few rows behind half a million without any: one workgroup of 512 threads less
+    than makes 2^32. With one document more the call is refused, and nothing written."""
+    some = Docs([5, 130], Hq=16, Hkv=16, D=D, seed=4)
+    # (rows / 128 + documents) * heads = 2^23 less one workgroup for each head
+    empty = [int(some.oq[0])] * ((1 << 19) - 1 - some.Tq // 128 - len(some.nq))
+    most, past = i32(empty + some.oq.tolist()), i32(empty + empty[:1] + some.oq.tolist())
+    args = dict(some.args, k_offsets=most)
+    out, lse = fq.attn_fwd(*some.dev, D, most, **args)
+    (want, tol), (wlse, ltol) = some.solve()
+    rows = slice(some.oq[0], some.oq[-1])
+    assert_within(f64(out)[rows], want[rows], tol[rows], "out")
+    assert_within(f64(lse)[:, rows], wlse[:, rows], ltol[:, rows], "lse")
+    sevens = [torch.full_like(t, 7.0) for t in some.dev]
+    if D > 128:  # (no gradients)
+        with pytest.raises(fq.Fp8rlError):
+            fq.attn_fwd(*some.dev, D, past, **dict(args, k_offsets=past), out=sevens[0])
+    else:
+        dout = some.dout.cuda()
+        grads = fq.attn_bwd(dout, *some.dev, out, lse, D, most, **args)
+        # the same without the empty documents: a key's queries in parts, and so other sums
+        same = fq.attn_bwd(dout, *some.dev, out, lse, D, some.q_offsets, **some.args)
+        for a, b in zip(grads, same):
+            assert (a[rows] - b[rows]).abs().max() <= 2.0 ** -7 * b[rows].abs().max()
+        with pytest.raises(fq.Fp8rlError):
+            fq.attn_bwd(dout, *some.dev, out, lse, D, past, **dict(args, k_offsets=past), dq=sevens[0],
+                        dk=sevens[1], dv=sevens[2])
+    assert all((t == 7).all() for t in sevens)
