@@ -123,7 +123,7 @@ fp8rl_status fp8rl_attn_decode(const fp8rl_attn_decode_args* args, void* workspa
   if (fp8rl_status s = check_cache_shape(c)) return s;
   if (fp8rl_status s = check_scores(a.sm_scale, a.window, a.cap)) return s;
   // (the units of all sequences are counted in 32 bits)
-  if (a.B * a.table_width >= (int64_t{1} << 35) / a.page_size) return FP8RL_ERR_SHAPE;
+  if (a.B * ((int64_t)a.table_width * a.page_size) >= int64_t{1} << 35) return FP8RL_ERR_SHAPE;
   if (a.B == 0) return FP8RL_OK;
   if (!a.q || !a.lengths || !a.out) return FP8RL_ERR_NULL;
   if (fp8rl_status s = check_cache(c)) return s;

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from fp8_blockwise_quantization_amd import _attn
-from tests.test_abi_attn_host import DOCS, ENULL, ESHAPE, EWS, L  # noqa: F401  (L: the fixture)
+from tests.test_abi_attn_host import A, CACHE, DOCS, ENULL, ESHAPE, EWS, L  # noqa: F401  (L: the fixture)
 
 
 def docs_args(**k):
@@ -63,3 +63,20 @@ def test_backward(L):  # noqa: F811
     # and the queries' rows do not count among these
     docs, T, heads = BELOW_24[1]
     assert call(docs, T, 100, heads, heads) == EWS
+
+
+@pytest.mark.parametrize("page_size", [1, 3, 16])
+def test_keys_of_all_sequences_of_a_decode(L, page_size):  # noqa: F811
+    """B * table_width * page_size < 2^35, also where the page size does not divide that."""
+    def call(B, width):
+        a = _attn.AttnDecodeArgs(**dict(CACHE, page_size=page_size, page_stride=page_size * 256, q=A,
+                                        ld_q=1024, B=B, q_heads=8, lengths=A, sm_scale=0.1, out=A,
+                                        ld_out=1024, table_width=width, ld_table=width))
+        return L.fp8rl_attn_decode(ctypes.byref(a), None, 0, None)
+
+    pages = -(-(1 << 35) // page_size)  # of 2^35 keys, or just past them
+    for B in (32, 43691, 65536):
+        width = (pages - 1) // B
+        if width * page_size <= 1 << 30:
+            assert call(B, width) == EWS, (B, width)
+        assert call(B, -(-pages // B)) == ESHAPE, (B, width)
