@@ -18,6 +18,10 @@
 // than 2300.) Where there are few keys, a key tile's queries are dealt out in parts, whose sums a
 // third kernel adds.
 //
+// P and dS go into their products as one bf16 term, 2^-8 of themselves at most: against 64 bits the
+// gradients are off by 0.0024 to 0.0026 of their norm, with float32 terms by 0.0018 to 0.0020. Second
+// terms would add three products to the seven.
+//
 // 8192 causal tokens, 32 query heads on 8 of 128: 770 us for dq, 1.07 PFLOP/s of its three
 // products, 1145 us for dk and dv, 0.96 of their four; 1.9 ms in all, 0.72 PFLOP/s of the five that
 // the gradients need. Memory: 2.1 GB read by the second pass, 1.9 TB/s.
@@ -261,7 +265,8 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnArgs d) {
   __shared__ __align__(1024) uint8_t s_mem[6 * kTile + kOwn * DP * 2];
   __shared__ __align__(1024) float s_row[3][2][kQueries];  // lse and delta of the tile's queries
   // the steps of the keys' operand that do not fit the registers beside the sums (spilled, their
-  // reloads would wait for the tiles in flight)
+  // reloads would wait for the tiles in flight: with MORE at 128 whole columns five registers still
+  // are)
   constexpr int kHeld = DP == 64 ? KS : MORE ? KS - 6 : KS - 4;
   __shared__ u32x4 s_k[4][KS - kHeld + 1][64];
   uint8_t* const s_v = s_mem + 6 * kTile;

@@ -18,12 +18,13 @@
 // the present one is worked on, and hands the 64-bit offset out through LDS.
 //
 // Bound by memory; every key and value is read once. Values go past the caches (nontemporal loads:
-// 64 uneven sequences of up to 4096 keys of 8 heads of 128 in E4M3, 57.8 us without, 53.1 with),
-// keys do not (their rows are read 64 bytes at a time, and the other half of a line was gone by the
-// next step: 35 us instead of 32 for a window of 1024 keys of 256). Those 64 sequences are 246 MB:
-// 47 us for this kernel, 5.2 TB/s, and 6 for the join; 529 MB, eight uneven sequences of up to
-// 32768 keys of 4 heads of 128 in bf16: 88 us, 6.0 TB/s, and 6. What lies beside the bytes is the
-// launch and the chain of lengths, table and first keys, about 4 us. Two tiles of keys under way in
+// 64 uneven sequences of up to 4096 keys of 8 heads of 128 in E4M3, 58.1 us without, 53.8 with; an
+// instruction takes their lines whole), keys do not (their rows are read 64 bytes at a time, and the
+// other half of a line was gone by the next step: 35 us instead of 32 for a window of 1024 keys of
+// 256). Those 64 sequences are 246 MB: 48 us for this kernel, 5.1 TB/s, and 6 for the join; 529 MB,
+// eight uneven sequences of up to 32768 keys of 4 heads of 128 in bf16: 88 us, 6.0 TB/s, and 6. What
+// lies beside the bytes is the launch and the chain of lengths, table and first keys, about 4 us. bf16
+// heads of 144 to 256 columns spill 23 to 48 registers. Two tiles of keys under way in
 // a wave (59.9 against 57.4 us: 16 waves' registers become 8's) and sixteen waves a CU with half a
 // piece each (69) were slower.
 #include "attn_ops.hpp"
@@ -34,11 +35,12 @@ namespace {
 
 constexpr int kWaves = 8;   // of a workgroup, and what a CU runs at once
 constexpr int kUnit = 32;   // keys of a wave's step
-// Keys, and their bytes in a head, up to which a sequence is not split. Uneven sequences of 32
-// query heads on 8 of 128 in E4M3, up to 1020 keys each, not split and split: one 9.8 and 13.0 us,
-// 64 of them 20.4 and 25.7; up to 1500 12.6 and 13.0, 27.7 and 29.8; up to 2040 16.6 and 13.2, both
-// 36. 1024 keys each of 8 heads of 256, one sequence and 100: in E4M3 16.2 and 17.3, 83.2 and 81.5;
-// in bf16 (twice these bytes) 38.8 and 29.2, 207 and 164.
+// Keys, and their bytes in a head, up to which a sequence is not split: one limit for heads of all
+// widths, below the crossing of narrow ones and above that of wide ones. Uneven sequences of 32 query
+// heads on 8 of 128 in E4M3, up to 1020 keys each, not split and split: one 9.7 and 12.1 us, 64 of
+// them 21.1 and 26.2; up to 1500 12.7 and 12.5, 28.8 and 30.5; up to 2040 17.1 and 12.7, both 37. 1024
+// keys each of 8 heads of 256, one sequence and 100: in E4M3 15.6 and 15.3, 88.9 and 82.8; in bf16
+// (twice these bytes, and so split) 33.2 and 26.4, 212 and 165.
 constexpr int kWhole = 1024;
 constexpr int kWholeBytes = 256 << 10;
 constexpr int kLeast = 2;   // units of a piece
@@ -106,9 +108,7 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& d, int lot, int la
   return {B, base, per};
 }
 
-// N 32-bit words at p, which is aligned to 8 bytes (4 for one word). ONCE: not kept in the caches
-// (for v, whose lines an instruction takes whole: 57.8 -> 53.8 us at 64 x 4096; k's come half a
-// line at a time, and some were read twice).
+// N 32-bit words at p, which is aligned to 8 bytes (4 for one word). ONCE: not kept in the caches.
 template <bool ONCE, int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
   typedef u32x4 __attribute__((aligned(8))) u32x4_8;

@@ -11,10 +11,13 @@
 //
 // Bound by the matrix cores and by what stands between their instructions: two waves on a SIMD, one
 // in its products while the other is in its exponentials. 8192 causal tokens, 32 query heads on 8
-// of 128: 550 us, 1.0 PFLOP/s, 48 % of the cycles in matrix instructions, no LDS bank conflicts; a
-// library product of 8192^3 reaches 1.29. Heads of 64: 0.83 PFLOP/s (half the products per
-// exponential), of 256: 0.78 (eight waves, all registers taken). Four tiles in LDS instead of two,
-// with eight waves, changed nothing: it is not the loads that a tile waits for.
+// of 128: 550 to 575 us a call from card to card (without a profiler), 1.0 PFLOP/s, 48 % of the
+// cycles in matrix instructions, no LDS bank conflicts; a library product of 8192^3 reaches 1.29. Heads
+// of 64: 0.83 PFLOP/s (half the products per exponential), of 256: 0.87 (eight waves, 17 of their
+// registers spilled), of 144 to 240: 0.29 (how many steps of q there are is not known to the compiler,
+// which leaves the loop over them as it is, and q in scratch memory: each step waits for its load).
+// Four tiles in LDS instead of two, with eight waves, changed nothing: it is not the loads that a tile
+// waits for.
 #include "attn_tile.hpp"
 
 namespace fp8rl {
@@ -31,7 +34,7 @@ constexpr int kFew = 512;
 
 }  // namespace
 
-// DP: head_dim rounded up to 64 or 128; PAD: it is less. MORE: capped scores or slopes. KH: waves
+// DP: head_dim rounded up to 64, 128 or 256; PAD: it is less. MORE: capped scores or slopes. KH: waves
 // that share 32 queries, each with its part of a tile's keys; their sums meet in the end.
 template <int DP, bool PAD, bool MORE, int KH>
 __global__ __launch_bounds__(256 * KH, 2) void attn_fwd_kernel(AttnArgs d) {
@@ -173,6 +176,9 @@ __global__ __launch_bounds__(256 * KH, 2) void attn_fwd_kernel(AttnArgs d) {
     const ColOperand<DP> vop(s_v + kOwn * part * DP * 2, lane);
 #pragma unroll
     for (int r = 0; r < 2 * NR; ++r) {
+      // (one bf16 term of a weight, 2^-8 of itself at most, at any size: against 64 bits out is off
+      // by 0.0019 to 0.0023 of its norm, with float32 weights by 0.0015 to 0.0017, the rounding of out
+      // itself. A second term would double these products.)
       const bf16x8 w = operand_of(s[r >> 1], r & 1);
 #pragma unroll
       for (int c = 0; c < DT; ++c) {

@@ -6,7 +6,7 @@
 // are 8 (i / 4) + 4h + i % 4 for i = 0 .. 15. The rows that a lane has of a result, eight by eight,
 // serve as the places of the next contraction (16 of them: 16s + {4h .. 4h + 3, 8 + 4h .. 8 + 4h +
 // 3}), so a result turns into an operand without leaving the lane, as long as the other operand
-// takes its places in the same order: operand_t does.
+// takes its places in the same order: ColOperand does.
 #pragma once
 
 #include "attn_ops.hpp"
@@ -45,7 +45,7 @@ struct DocTile {
   int64_t q0, k0;  // its first row of q, of k and v
 };
 
-// The tile that comes at place `index` of the launch's a.slots.
+// The tile that comes at place `index` of the launch's args.slots.
 //
 // Up to 64 documents: tiles that take longest first, so that the last ones to run are short. A tile
 // of queries goes through the keys in front of it, one of keys through the queries behind it; with
